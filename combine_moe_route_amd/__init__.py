@@ -20,11 +20,14 @@ _API = (
     "moe_dispatch_max_rows",
     "moe_dispatch_no_alloc",
     "moe_dispatch_workspace_bytes",
+    "moe_gated_act_quant_fp8",
+    "moe_grouped_gemm_bf16",
     "moe_grouped_gemm_fp8",
     "moe_grouped_gemm_workspace_bytes",
     "moe_harness_expert_scale",
     "moe_route_dispatch",
     "moe_route_replicas",
+    "moe_route_scored",
     "moe_route_topk",
     "moe_route_topk_shared",
     "status_string",

@@ -21,12 +21,16 @@ LIB_PATH = os.environ.get("MOE_ROUTE_LIB", os.path.join(_HERE, "libmoeroute.so")
 MOE_OK, MOE_EINVAL, MOE_ENOSPC, MOE_EALIGN, MOE_EHIP, MOE_ENULL = 0, -1, -2, -3, -4, -5
 MOE_OUT_BF16, MOE_OUT_FP8_E4M3 = 0, 1
 MOE_MAX_EXPERTS = 1024
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+MOE_LOGITS = {torch.float32: 0, torch.bfloat16: 1}
+MOE_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 MOE_NO_ALLOC_SCRATCH_BYTES = 16 << 20
 
 # every symbol include/moe_route.h declares
 EXPORTS = (
     "moe_route_topk",
     "moe_route_topk_shared",
+    "moe_route_scored",
     "moe_route_replicas",
     "moe_dispatch_max_rows",
     "moe_dispatch_workspace_bytes",
@@ -38,6 +42,8 @@ EXPORTS = (
     "moe_combine_recv",
     "moe_grouped_gemm_workspace_bytes",
     "moe_grouped_gemm_fp8",
+    "moe_grouped_gemm_bf16",
+    "moe_gated_act_quant_fp8",
     "moe_harness_expert_scale",
     "moe_status_string",
 )
@@ -86,6 +92,14 @@ def _load() -> ctypes.CDLL:
     lib.moe_grouped_gemm_fp8.argtypes = [P, P, P, P, P, i32, i32, i32, i64, P, P,
                                          ctypes.c_size_t, P]
     lib.moe_grouped_gemm_fp8.restype = i32
+    f32 = ctypes.c_float
+    lib.moe_route_scored.argtypes = [P, i32, i64, i64, i32, i32, i32, P, i32, i32, i32, i32, f32,
+                                     i32, f32, P, P, P]
+    lib.moe_route_scored.restype = i32
+    lib.moe_grouped_gemm_bf16.argtypes = [P, P, P, P, P, i32, i32, i32, i64, i32, i32, P, P]
+    lib.moe_grouped_gemm_bf16.restype = i32
+    lib.moe_gated_act_quant_fp8.argtypes = [P, P, i32, i64, i32, i32, P, P, P]
+    lib.moe_gated_act_quant_fp8.restype = i32
     lib.moe_harness_expert_scale.argtypes = [P, P, P, P, P, i64, i32, i32, i32, i32, P, P]
     lib.moe_harness_expert_scale.restype = i32
     lib.moe_status_string.argtypes = [i32]
@@ -163,6 +177,55 @@ def moe_route_topk_shared(logits: torch.Tensor, k: int, n_shared: int, shared_w:
     _check("moe_route_topk_shared", lib.moe_route_topk_shared(
         _ptr(logits), T, E, k, n_shared, float(shared_w), _ptr(topk_idx), _ptr(topk_w),
         _stream(dev)))
+    return topk_idx, topk_w
+
+
+def _choice(table: dict, key, name: str) -> int:
+    if key not in table:
+        raise ValueError(f"{name}: {key!r}, expected one of {list(table)}")
+    return table[key]
+
+
+def moe_route_scored(logits: torch.Tensor, k: int, score: str = "sigmoid",
+                     bias: Optional[torch.Tensor] = None, n_group: int = 1, topk_group: int = 1,
+                     group_top: int = 2, renorm: bool = True, scale: float = 1.0,
+                     n_shared: int = 0, shared_w: float = 1.0,
+                     topk_idx: Optional[torch.Tensor] = None,
+                     topk_w: Optional[torch.Tensor] = None):
+    """Scored router gate: sigmoid or softmax scores, balance bias fp32 [E] in
+    the choice only, the best topk_group of n_group expert groups (each by the
+    sum of its group_top best), top-k, weights renormalised and scaled:
+    (topk_idx int32 [T,k+n_shared], topk_w float32 [T,k+n_shared]); slots
+    without an expert (all else masked by -inf) hold -1 and 0. logits: float32
+    or bfloat16 [T,E], rows may be strided."""
+    if logits.dtype not in MOE_LOGITS:
+        raise TypeError(f"logits: dtype {logits.dtype}, expected float32 or bfloat16")
+    if not logits.is_cuda:
+        raise TypeError("logits: must be a GPU tensor")
+    if logits.dim() != 2:
+        raise ValueError(f"logits: shape {tuple(logits.shape)}, expected (T, E)")
+    T, E = logits.shape
+    ld = logits.stride(0)
+    if T <= 1:      # a single row has no row stride (torch may report any)
+        ld = E
+    if (E > 1 and logits.stride(1) != 1) or ld < E:
+        raise ValueError(f"logits: strides {logits.stride()}, expected (>= E, 1)")
+    dev = logits.device
+    ks = k + n_shared
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,), dev)
+    if topk_idx is None:
+        topk_idx = torch.empty((T, ks), dtype=torch.int32, device=dev)
+    if topk_w is None:
+        topk_w = torch.empty((T, ks), dtype=torch.float32, device=dev)
+    _need(topk_idx, "topk_idx", torch.int32, (T, ks), dev)
+    _need(topk_w, "topk_w", torch.float32, (T, ks), dev)
+    with torch.cuda.device(dev):
+        _check("moe_route_scored", lib.moe_route_scored(
+            _ptr(logits), MOE_LOGITS[logits.dtype], ld, T, E, k,
+            _choice(MOE_SCORES, score, "score"), _ptr(bias), n_group, topk_group, group_top,
+            int(renorm), float(scale), n_shared, float(shared_w), _ptr(topk_idx), _ptr(topk_w),
+            _stream(dev)))
     return topk_idx, topk_w
 
 
@@ -445,3 +508,66 @@ def moe_grouped_gemm_fp8(a: torch.Tensor, a_scales: torch.Tensor, expert_offsets
         _ptr(a), _ptr(a_scales), _ptr(expert_offsets), _ptr(w), _ptr(w_scales), E, N, K, R,
         _ptr(y), _ptr(workspace), workspace.numel(), _stream(dev)))
     return y
+
+
+def moe_grouped_gemm_bf16(a: torch.Tensor, expert_offsets: torch.Tensor, w: torch.Tensor,
+                          bias: Optional[torch.Tensor] = None, act: str = "none",
+                          gated: bool = False, residual: Optional[torch.Tensor] = None,
+                          y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """bf16 grouped GEMM over the dispatch segments with its epilogue: with
+    z = a w[e]^T + bias[e], y = act(z) + residual [max_rows, N], or gated
+    y = act(z[:, :N/2]) * z[:, N/2:] + residual [max_rows, N/2]. Rows of no
+    segment are left as they were. a: bfloat16 [max_rows, K], w: bfloat16
+    [E, N, K], bias: bfloat16 [E, N]; residual may be y itself."""
+    _need(a, "a", torch.bfloat16)
+    dev = a.device
+    _need(w, "w", torch.bfloat16, None, dev)
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError(f"a, w: shapes {tuple(a.shape)}, {tuple(w.shape)}, "
+                         "expected (max_rows, K), (E, N, K)")
+    R, K = a.shape
+    E, N, Kw = w.shape
+    if Kw != K:
+        raise ValueError(f"w: inner size {Kw}, expected {K}")
+    n_out = N // 2 if gated else N
+    _need(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev)
+    if bias is not None:
+        _need(bias, "bias", torch.bfloat16, (E, N), dev)
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, (R, n_out), dev)
+    if y is None:
+        y = torch.empty((R, n_out), dtype=torch.bfloat16, device=dev)
+    _need(y, "y", torch.bfloat16, (R, n_out), dev)
+    with torch.cuda.device(dev):
+        _check("moe_grouped_gemm_bf16", lib.moe_grouped_gemm_bf16(
+            _ptr(a), _ptr(expert_offsets), _ptr(w), _ptr(bias), _ptr(residual), E, N, K, R,
+            _choice(MOE_ACTS, act, "act"), int(gated), _ptr(y), _stream(dev)))
+    return y
+
+
+# ----------------------------------------------------------------- between the FP8 products
+
+def moe_gated_act_quant_fp8(h: torch.Tensor, expert_offsets: torch.Tensor, act: str = "silu",
+                            out: Optional[torch.Tensor] = None,
+                            out_scales: Optional[torch.Tensor] = None):
+    """act(h[:, :I]) * h[:, I:] of the rows below expert_offsets[E], quantised:
+    (out uint8 E4M3 codes [max_rows, I], out_scales float32 [max_rows, I/128]),
+    the operands of the next moe_grouped_gemm_fp8. h: bfloat16 [max_rows, 2I].
+    Rows behind the last segment are left as they were."""
+    _need(h, "h", torch.bfloat16)
+    dev = h.device
+    if h.dim() != 2 or h.shape[1] % 2:
+        raise ValueError(f"h: shape {tuple(h.shape)}, expected (max_rows, 2 I)")
+    R, I = h.shape[0], h.shape[1] // 2
+    _need(expert_offsets, "expert_offsets", torch.int32, None, dev)
+    if out is None:
+        out = torch.empty((R, I), dtype=torch.uint8, device=dev)
+    if out_scales is None:
+        out_scales = torch.empty((R, I // 128), dtype=torch.float32, device=dev)
+    _need(out, "out", torch.uint8, (R, I), dev)
+    _need(out_scales, "out_scales", torch.float32, (R, I // 128), dev)
+    with torch.cuda.device(dev):
+        _check("moe_gated_act_quant_fp8", lib.moe_gated_act_quant_fp8(
+            _ptr(h), _ptr(expert_offsets), expert_offsets.numel() - 1, R, I,
+            _choice(MOE_ACTS, act, "act"), _ptr(out), _ptr(out_scales), _stream(dev)))
+    return out, out_scales

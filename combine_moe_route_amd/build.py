@@ -11,8 +11,8 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoeroute.so")
-SOURCES = ["api.hip", "route_topk.hip", "dispatch.hip", "combine.hip", "combine_sender.hip",
-           "grouped_gemm.hip"]
+SOURCES = ["api.hip", "route_topk.hip", "route_scored.hip", "dispatch.hip", "combine.hip",
+           "combine_sender.hip", "grouped_gemm.hip", "grouped_gemm_bf16.hip", "gated_act.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

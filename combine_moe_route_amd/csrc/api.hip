@@ -382,6 +382,106 @@ int moe_grouped_gemm_fp8(const void* a, const float* a_scales, const int32_t* ex
     return status_of(e);
 }
 
+int moe_route_scored(const void* logits, int logits_dtype, int64_t ld_logits, int64_t T, int E,
+                     int k, int score, const float* bias, int n_group, int topk_group,
+                     int group_top, int renorm, float scale, int n_shared, float shared_w,
+                     int32_t* topk_idx, float* topk_w, void* stream) {
+    if (T < 0 || T > kInt32Max || k < 1 || E < k || n_shared < 0 || n_shared > MOE_MAX_EXPERTS ||
+        E > MOE_MAX_EXPERTS - n_shared)
+        return MOE_EINVAL;
+    if (logits_dtype != MOE_LOGITS_F32 && logits_dtype != MOE_LOGITS_BF16) return MOE_EINVAL;
+    if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_EINVAL;
+    if (n_group < 1 || n_group > E || E % n_group != 0) return MOE_EINVAL;
+    if (topk_group < 1 || topk_group > n_group || k > topk_group * (E / n_group)) return MOE_EINVAL;
+    if (group_top != 1 && group_top != 2) return MOE_EINVAL;
+    if (ld_logits < E || ld_logits > ((int64_t)1 << 31) || T * ld_logits > ((int64_t)1 << 40))
+        return MOE_EINVAL;
+    if (T * (int64_t)(k + n_shared) > kInt32Max) return MOE_EINVAL;
+    moe::ScoredArgs a;
+    a.logits = logits;
+    a.bias = bias;
+    a.topk_idx = topk_idx;
+    a.topk_w = topk_w;
+    a.T = T;
+    a.ld = ld_logits;
+    a.E = E;
+    a.k = k;
+    a.n_group = n_group;
+    a.topk_group = topk_group;
+    a.group_top = group_top;
+    a.n_shared = n_shared;
+    a.scale = scale;
+    a.shared_w = shared_w;
+    a.bf16 = logits_dtype == MOE_LOGITS_BF16;
+    a.sigmoid = score == MOE_SCORE_SIGMOID;
+    a.renorm = renorm != 0;
+    moe::LaunchInfo info;
+    (void)moe::launch_route_scored(a, nullptr, &info, false);
+    if (!all_fit(&info, 1)) return MOE_EINVAL;
+    if (T == 0) return MOE_OK;
+    if (!logits || !topk_idx || !topk_w) return MOE_ENULL;
+    if (!aligned(logits, a.bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(topk_idx, 4) ||
+        !aligned(topk_w, 4))
+        return MOE_EALIGN;
+    const hipError_t e = moe::launch_route_scored(a, static_cast<hipStream_t>(stream), &info);
+    if (log_enabled()) log_launch(info.name, info);
+    return status_of(e);
+}
+
+int moe_grouped_gemm_bf16(const void* a, const int32_t* expert_offsets, const void* w,
+                          const void* bias, const void* residual, int E, int N, int K,
+                          int64_t max_rows, int act, int gated, void* y, void* stream) {
+    if (E < 1 || E > MOE_MAX_EXPERTS || max_rows < 0 || max_rows > kInt32Max) return MOE_EINVAL;
+    if (K < 8 || K > (1 << 20) || K % 8 != 0) return MOE_EINVAL;
+    if (N < 8 || N > (1 << 20) || N % (gated ? 16 : 8) != 0) return MOE_EINVAL;
+    if (act < MOE_ACT_NONE || act > MOE_ACT_GELU) return MOE_EINVAL;
+    moe::GemmBf16Args g;
+    g.a = static_cast<const uint16_t*>(a);
+    g.off = expert_offsets;
+    g.w = static_cast<const uint16_t*>(w);
+    g.bias = static_cast<const uint16_t*>(bias);
+    g.residual = static_cast<const uint16_t*>(residual);
+    g.y = static_cast<uint16_t*>(y);
+    g.max_rows = max_rows;
+    g.E = E;
+    g.N = N;
+    g.K = K;
+    g.act = act;
+    g.gated = gated != 0;
+    moe::LaunchInfo info;
+    (void)moe::launch_grouped_gemm_bf16(g, nullptr, &info, false);
+    if (!all_fit(&info, 1)) return MOE_EINVAL;
+    if (max_rows == 0) return MOE_OK;
+    if (!a || !expert_offsets || !w || !y) return MOE_ENULL;
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(bias, 16) ||
+        !aligned(residual, 16) || !aligned(expert_offsets, 4))
+        return MOE_EALIGN;
+    const hipError_t e = moe::launch_grouped_gemm_bf16(g, static_cast<hipStream_t>(stream), &info);
+    if (log_enabled()) log_launch(info.name, info);
+    return status_of(e);
+}
+
+int moe_gated_act_quant_fp8(const void* h, const int32_t* expert_offsets, int E, int64_t max_rows,
+                            int I, int act, void* out, float* out_scales, void* stream) {
+    if (E < 1 || E > MOE_MAX_EXPERTS || max_rows < 0 || max_rows > kInt32Max) return MOE_EINVAL;
+    if (I < 128 || I > (1 << 20) || I % 128 != 0) return MOE_EINVAL;
+    if (act < MOE_ACT_NONE || act > MOE_ACT_GELU) return MOE_EINVAL;
+    moe::LaunchInfo info;
+    (void)moe::launch_gated_act_fp8(h, expert_offsets, E, max_rows, I, act, out, out_scales,
+                                    nullptr, &info, false);
+    if (!all_fit(&info, 1)) return MOE_EINVAL;
+    if (max_rows == 0) return MOE_OK;
+    if (!h || !expert_offsets || !out || !out_scales) return MOE_ENULL;
+    if (!aligned(h, 16) || !aligned(out, 16) || !aligned(out_scales, 4) ||
+        !aligned(expert_offsets, 4))
+        return MOE_EALIGN;
+    const hipError_t e = moe::launch_gated_act_fp8(h, expert_offsets, E, max_rows, I, act, out,
+                                                   out_scales, static_cast<hipStream_t>(stream),
+                                                   &info);
+    if (log_enabled()) log_launch(info.name, info);
+    return status_of(e);
+}
+
 const char* moe_status_string(int status) {
     switch (status) {
         case MOE_OK: return "ok";

@@ -108,4 +108,38 @@ hipError_t launch_grouped_gemm_fp8(const void* a, const float* a_scales,
                                    void* y, void* workspace, hipStream_t stream,
                                    LaunchInfo info[2], bool run = true);
 
+// Scored router gate (moe_route_scored).
+struct ScoredArgs {
+    const void* logits;          // [T, E], rows ld apart; fp32 or bf16
+    const float* bias;           // [E] or nullptr
+    int32_t* topk_idx;
+    float* topk_w;
+    int64_t T, ld;
+    int E, k, n_group, topk_group, group_top, n_shared;
+    float scale, shared_w;
+    bool bf16, sigmoid, renorm;
+};
+hipError_t launch_route_scored(const ScoredArgs& a, hipStream_t stream, LaunchInfo* info,
+                               bool run = true);
+
+// bf16 grouped GEMM with its epilogue (moe_grouped_gemm_bf16).
+struct GemmBf16Args {
+    const uint16_t* a;
+    const int32_t* off;
+    const uint16_t* w;
+    const uint16_t* bias;        // [E, N] or nullptr
+    const uint16_t* residual;    // [max_rows, N or N/2] or nullptr
+    uint16_t* y;
+    int64_t max_rows;
+    int E, N, K, act;
+    bool gated;
+};
+hipError_t launch_grouped_gemm_bf16(const GemmBf16Args& g, hipStream_t stream, LaunchInfo* info,
+                                    bool run = true);
+
+// Gated activation with FP8 quantisation (moe_gated_act_quant_fp8).
+hipError_t launch_gated_act_fp8(const void* h, const int32_t* expert_offsets, int E,
+                                int64_t max_rows, int I, int act, void* out, float* out_scales,
+                                hipStream_t stream, LaunchInfo* info, bool run = true);
+
 }  // namespace moe

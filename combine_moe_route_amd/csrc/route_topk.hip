@@ -32,48 +32,6 @@
 
 namespace moe {
 
-namespace {
-
-constexpr int kDppRowMirror = 0x140;   // lane i <-> 15-i within each row of 16
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
-}
-
-// Butterfly over aligned groups of S lanes; OP(a, b) must be commutative and
-// associative. Every lane of a group ends with the group's result.
-template <int S, typename F>
-__device__ __forceinline__ uint32_t group_reduce(uint32_t v, F op) {
-    if (S > 1) v = op(v, dpp_u32<kDppQuadXor1>(v));
-    if (S > 2) v = op(v, dpp_u32<kDppQuadXor2>(v));
-    if (S > 4) v = op(v, dpp_u32<kDppRowHalfMirror>(v));
-    if (S > 8) v = op(v, dpp_u32<kDppRowMirror>(v));
-    if (S > 16) {
-        const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-        v = op(p[0], p[1]);
-    }
-    if (S > 32) {
-        const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-        v = op(p[0], p[1]);
-    }
-    return v;
-}
-
-struct UMax {
-    __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
-};
-struct UMin {
-    __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a < b ? a : b; }
-};
-struct FAdd {
-    __device__ uint32_t operator()(uint32_t a, uint32_t b) const {
-        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-    }
-};
-
-}  // namespace
-
 constexpr int kRouteThreads = 256;
 
 template <int S, int NV>

@@ -93,6 +93,48 @@ int moe_route_topk_shared(const float* logits, int64_t T, int E, int k, int n_sh
                           float shared_w, int32_t* topk_idx, float* topk_w, void* stream);
 
 /*
+ * Scored router gate: sigmoid or softmax scores, a balance bias that enters
+ * the choice but not the weights, a choice limited to the best groups of
+ * experts, top-k, and weights from the scores of the chosen experts.
+ *
+ *   s[t,e] = fp32(sigmoid(l)) or fp32(exp(l - m) / sum_e exp(l - m)), each
+ *            rounded to fp32 once (computed in fp64)
+ *   key    = s[t,e] + bias[e] (fp32); bias NULL: s[t,e]
+ *   groups = group g is experts [g*E/n_group, (g+1)*E/n_group), scored by the
+ *            fp32 sum of its group_top best keys (all it has, if fewer are
+ *            live); the topk_group groups of highest score stay, equal
+ *            scores the lower group first. n_group == topk_group: no limit
+ *   chosen = the k highest keys of the groups that stay, descending, equal
+ *            keys the lower expert first
+ *   w      = s of the chosen expert; with renorm divided by the fp32 sum over
+ *            the chosen (0 when that sum is 0); then times scale
+ *
+ * Masks: an expert whose logit, or whose key, is -inf or NaN is never chosen
+ * for that token (softmax gives it no mass); +inf counts as the largest
+ * finite fp32 in the softmax. When fewer than k experts are left, the last
+ * slots hold expert -1 with weight 0, which moe_dispatch drops and
+ * moe_combine skips: a token whose logits are all -inf is routed nowhere.
+ *
+ *   logits       device, fp32 or bf16 (logits_dtype) [T, E], rows ld_logits
+ *                elements apart (>= E); aligned to its element
+ *   bias         device, fp32 [E], or NULL
+ *   n_shared     always-chosen experts E .. E+n_shared-1 with weight shared_w
+ *                in slots k .. k+n_shared-1, as in moe_route_topk_shared
+ *   topk_idx     device, int32 [T, k + n_shared] out
+ *   topk_w       device, fp32 [T, k + n_shared] out
+ *   1 <= k <= topk_group * E / n_group; E % n_group == 0;
+ *   1 <= topk_group <= n_group; group_top 1 or 2;
+ *   E + n_shared <= MOE_MAX_EXPERTS; T >= 0 (T == 0 is a no-op).
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef enum { MOE_LOGITS_F32 = 0, MOE_LOGITS_BF16 = 1 } moe_logits_dtype;
+
+int moe_route_scored(const void* logits, int logits_dtype, int64_t ld_logits, int64_t T, int E,
+                     int k, int score, const float* bias, int n_group, int topk_group,
+                     int group_top, int renorm, float scale, int n_shared, float shared_w,
+                     int32_t* topk_idx, float* topk_w, void* stream);
+
+/*
  * Redundant expert replicas (DeepSeek-V3 excerpts: heavily loaded experts get
  * extra copies hosted as separate experts). In place on topk_idx [T, k]:
  * logical expert e owns physical experts replica_base[e] ..
@@ -323,6 +365,69 @@ int moe_grouped_gemm_fp8(const void* a, const float* a_scales, const int32_t* ex
                          const void* w, const float* w_scales, int E, int N, int K,
                          int64_t max_rows, void* y, void* workspace, size_t workspace_bytes,
                          void* stream);
+
+/* Activations of the experts, in fp32: none, max(z, 0), z * sigmoid(z),
+ * z/2 * erfc(-z/sqrt 2). */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 } moe_act;
+
+/*
+ * Grouped GEMM over the bf16 segments, with its epilogue. For every expert e
+ * and every row r in [expert_offsets[e], expert_offsets[e+1]):
+ *
+ *   z[n]  = sum_k a[r, k] * w[e, n, k] + bias[e, n]       (fp32)
+ *   plain:  y[r, n] = bf16( act(z[n]) + residual[r, n] ),               n < N
+ *   gated:  y[r, n] = bf16( act(z[n]) * z[N/2 + n] + residual[r, n] ),  n < N/2
+ *
+ * with one rounding (nearest even) at the end; the order of the fp32 sum over
+ * k is not fixed by the interface, and repeats for the same arguments. Gate
+ * rows of w come first, up rows second. With E = 1 and offsets {0, rows} it
+ * is a linear layer with the same epilogue (a shared expert added to what
+ * moe_combine gave: residual = combine's y).
+ *
+ *   a               device bf16 [max_rows, K], 16-byte aligned: moe_dispatch's
+ *                   out in bf16 mode, or the y of a product before
+ *   expert_offsets  device int32 [E+1]: moe_dispatch's expert_offsets (any
+ *                   row_align). Segment bounds are clamped to [0, max_rows]
+ *   w               device bf16 [E, N, K], K contiguous, 16-byte aligned
+ *   bias            device bf16 [E, N], 16-byte aligned, or NULL
+ *   residual        device bf16 [max_rows, N or N/2], 16-byte aligned, or NULL;
+ *                   may be y itself (y += ...), and may not overlap it otherwise
+ *   y               device bf16 [max_rows, N or N/2] out, 16-byte aligned.
+ *                   Rows of no segment are not written, and rows of a or
+ *                   residual in no segment are not read.
+ *   E, N, K         1 <= E <= 1024; 8 <= K <= 2^20, K % 8 == 0;
+ *                   8 <= N <= 2^20, N % 8 == 0 (N % 16 == 0 when gated)
+ *   max_rows        rows of a, residual and y; 0 <= max_rows < 2^31
+ * y overlaps neither a nor w. No workspace; nothing is kept between calls.
+ * Errors: MOE_EINVAL (limits, launch size), MOE_ENULL, MOE_EALIGN, MOE_EHIP.
+ * max_rows == 0 returns MOE_OK without a launch.
+ */
+int moe_grouped_gemm_bf16(const void* a, const int32_t* expert_offsets, const void* w,
+                          const void* bias, const void* residual, int E, int N, int K,
+                          int64_t max_rows, int act, int gated, void* y, void* stream);
+
+/*
+ * Gated activation between the two FP8 grouped GEMMs. For every row r below
+ * expert_offsets[E] (clamped to max_rows) and block b of 128 channels:
+ *
+ *   v[c]  = act(h[r, c]) * h[r, I + c]                    (fp32)
+ *   s     = max |v| over the block / 448                  (fp32)
+ *   out   = E4M3 codes of v / s, nearest even, saturated to +-448; a block
+ *           whose s is 0 gets zero codes (moe_dispatch's quantisation)
+ *
+ *   h               device bf16 [max_rows, 2 I], 16-byte aligned, finite: the
+ *                   y of moe_grouped_gemm_fp8 with N = 2 I (gate, then up)
+ *   expert_offsets  device int32 [E+1]: moe_dispatch's; only [E] is read
+ *   out             device E4M3 [max_rows, I] out, 16-byte aligned
+ *   out_scales      device fp32 [max_rows, I/128] out
+ *   I % 128 == 0, 128 <= I <= 2^20; 0 <= max_rows < 2^31; 1 <= E <= 1024
+ * out and out_scales are the a and a_scales of the next moe_grouped_gemm_fp8.
+ * Rows at or past expert_offsets[E] are neither read nor written; pad rows
+ * of a segment (zeros) give zero codes and scales. max_rows == 0 returns
+ * MOE_OK without a launch.
+ */
+int moe_gated_act_quant_fp8(const void* h, const int32_t* expert_offsets, int E, int64_t max_rows,
+                            int I, int act, void* out, float* out_scales, void* stream);
 
 /*
  * Stand-in experts for tests and the benchmark (not part of the path):
