@@ -127,6 +127,23 @@ def _stream(device: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _run(name: str, dev: torch.device, *args):
+    """lib.<name>(*args, stream) on torch's current stream of `dev`, with that
+    device current; a non-zero status raises. Tensors go as addresses."""
+    fn = getattr(lib, name)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if status != MOE_OK:
+        raise MoeRouteError(name, status)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _need(t: torch.Tensor, name: str, dtype, shape=None, device=None):
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -220,12 +237,9 @@ def moe_route_scored(logits: torch.Tensor, k: int, score: str = "sigmoid",
         topk_w = torch.empty((T, ks), dtype=torch.float32, device=dev)
     _need(topk_idx, "topk_idx", torch.int32, (T, ks), dev)
     _need(topk_w, "topk_w", torch.float32, (T, ks), dev)
-    with torch.cuda.device(dev):
-        _check("moe_route_scored", lib.moe_route_scored(
-            _ptr(logits), MOE_LOGITS[logits.dtype], ld, T, E, k,
-            _choice(MOE_SCORES, score, "score"), _ptr(bias), n_group, topk_group, group_top,
-            int(renorm), float(scale), n_shared, float(shared_w), _ptr(topk_idx), _ptr(topk_w),
-            _stream(dev)))
+    _run("moe_route_scored", dev, logits.data_ptr(), MOE_LOGITS[logits.dtype], ld, T, E, k,
+         _choice(MOE_SCORES, score, "score"), _addr(bias), n_group, topk_group, group_top,
+         int(renorm), scale, n_shared, shared_w, topk_idx.data_ptr(), topk_w.data_ptr())
     return topk_idx, topk_w
 
 
@@ -538,10 +552,9 @@ def moe_grouped_gemm_bf16(a: torch.Tensor, expert_offsets: torch.Tensor, w: torc
     if y is None:
         y = torch.empty((R, n_out), dtype=torch.bfloat16, device=dev)
     _need(y, "y", torch.bfloat16, (R, n_out), dev)
-    with torch.cuda.device(dev):
-        _check("moe_grouped_gemm_bf16", lib.moe_grouped_gemm_bf16(
-            _ptr(a), _ptr(expert_offsets), _ptr(w), _ptr(bias), _ptr(residual), E, N, K, R,
-            _choice(MOE_ACTS, act, "act"), int(gated), _ptr(y), _stream(dev)))
+    _run("moe_grouped_gemm_bf16", dev, a.data_ptr(), expert_offsets.data_ptr(), w.data_ptr(),
+         _addr(bias), _addr(residual), E, N, K, R, _choice(MOE_ACTS, act, "act"), int(gated),
+         y.data_ptr())
     return y
 
 
@@ -566,8 +579,7 @@ def moe_gated_act_quant_fp8(h: torch.Tensor, expert_offsets: torch.Tensor, act: 
         out_scales = torch.empty((R, I // 128), dtype=torch.float32, device=dev)
     _need(out, "out", torch.uint8, (R, I), dev)
     _need(out_scales, "out_scales", torch.float32, (R, I // 128), dev)
-    with torch.cuda.device(dev):
-        _check("moe_gated_act_quant_fp8", lib.moe_gated_act_quant_fp8(
-            _ptr(h), _ptr(expert_offsets), expert_offsets.numel() - 1, R, I,
-            _choice(MOE_ACTS, act, "act"), _ptr(out), _ptr(out_scales), _stream(dev)))
+    _run("moe_gated_act_quant_fp8", dev, h.data_ptr(), expert_offsets.data_ptr(),
+         expert_offsets.numel() - 1, R, I, _choice(MOE_ACTS, act, "act"), out.data_ptr(),
+         out_scales.data_ptr())
     return out, out_scales

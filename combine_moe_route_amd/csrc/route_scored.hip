@@ -13,6 +13,10 @@
 // the choice are often a few fp32 units apart, so a score that is one unit
 // off would choose another expert. After that rounding the choice is exact
 // fp32 comparisons and additions, ties to the lower index.
+//
+// Two kernels, both with k rounds of a maximum over the lanes of a token:
+// k_route_chunks for rows of up to 256 chunks of four experts and k up to its
+// lanes per token, k_route_rounds for every other shape.
 #include "launch.h"
 #include "moe_device.h"
 
@@ -28,9 +32,53 @@ __device__ __forceinline__ float load_logit(const void* p, bool bf16, int64_t i)
     return static_cast<const float*>(p)[i];
 }
 
-struct DAdd {
-    __device__ double operator()(double a, double b) const { return a + b; }
+struct FMax {
+    __device__ uint32_t operator()(uint32_t a, uint32_t b) const {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }
 };
+
+// exp(y) in fp64 for |y| <= 150: y = n ln 2 + r with |r| <= ln 2 / 2 (Cody and
+// Waite's reduction, ln 2 in two parts), the Taylor series of exp(r) to r^12 / 12! (the next term is below 2^-52), times 2^n.
+// A score rounded to fp32 from it differs from the right rounding only where
+// the exact value lies within about 2^-51 of a midpoint between two floats,
+// once in 2^25 values.
+__device__ __forceinline__ double exp64(double y) {
+    const double n = rint(y * 1.4426950408889634);
+    double r = fma(n, -0.69314718055994530942, y);       // ln 2 as a double,
+    r = fma(n, -2.3190468138462996e-17, r);              // and what it lacks
+    double p = 2.08767569878680989792e-09;               // 1 / 12!
+    p = fma(p, r, 2.50521083854417187751e-08);
+    p = fma(p, r, 2.75573192239858906526e-07);
+    p = fma(p, r, 2.75573192239858906526e-06);
+    p = fma(p, r, 2.48015873015873015873e-05);
+    p = fma(p, r, 1.98412698412698412698e-04);
+    p = fma(p, r, 1.38888888888888888889e-03);
+    p = fma(p, r, 8.33333333333333333333e-03);
+    p = fma(p, r, 4.16666666666666666667e-02);
+    p = fma(p, r, 1.66666666666666666667e-01);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    return ldexp(p, (int)n);
+}
+
+// 1 / d for d in [1, 2^220]: the hardware's estimate and two Newton steps.
+__device__ __forceinline__ double recip64(double d) {
+    double q = __builtin_amdgcn_rcp(d);
+    q = fma(fma(-d, q, 1.0), q, q);
+    return fma(fma(-d, q, 1.0), q, q);
+}
+
+// Beyond +-150 the score is 0 or 1 in fp32 already.
+__device__ __forceinline__ float sigmoid32(float l) {
+    return (float)recip64(1.0 + exp64(-(double)__builtin_amdgcn_fmed3f(l, -150.0f, 150.0f)));
+}
+
+// exp(l - m) for l <= m; below exp(-150) nothing reaches an fp32 score
+__device__ __forceinline__ double exp_diff(float l, float m) {
+    return exp64(fmax((double)l - (double)m, -150.0));
+}
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
@@ -49,7 +97,7 @@ __device__ __forceinline__ uint32_t choice_key(float v) {
 // LDS per wave: scores [E], keys [E] (reused by the group stage), chosen
 // experts [k], group keys [n_group].
 template <int NV>
-__global__ __launch_bounds__(kScoredThreads) void k_route_scored(ScoredArgs a) {
+__global__ __launch_bounds__(kScoredThreads) void k_route_rounds(ScoredArgs a) {
     extern __shared__ uint32_t s_mem[];
     const int lane = threadIdx.x & (kWave - 1);
     const int wid = threadIdx.x / kWave;
@@ -72,7 +120,7 @@ __global__ __launch_bounds__(kScoredThreads) void k_route_scored(ScoredArgs a) {
     float s[NV];
     if (a.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < NV; i++) s[i] = (float)(1.0 / (1.0 + exp(-(double)l[i])));
+        for (int i = 0; i < NV; i++) s[i] = sigmoid32(l[i]);
     } else {
         float m = -INFINITY;
 #pragma unroll
@@ -85,12 +133,13 @@ __global__ __launch_bounds__(kScoredThreads) void k_route_scored(ScoredArgs a) {
         double p[NV], sum = 0.0;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            p[i] = l[i] > -INFINITY ? exp((double)l[i] - (double)m) : 0.0;
+            p[i] = l[i] > -INFINITY ? exp_diff(l[i], m) : 0.0;
             sum += p[i];
         }
         sum = wave_sum_f64(sum);
+        const double inv = sum > 0.0 ? recip64(sum) : 0.0;
 #pragma unroll
-        for (int i = 0; i < NV; i++) s[i] = sum > 0.0 ? (float)(p[i] / sum) : 0.0f;
+        for (int i = 0; i < NV; i++) s[i] = (float)(p[i] * inv);
     }
     uint32_t c[NV];
 #pragma unroll
@@ -170,19 +219,366 @@ __global__ __launch_bounds__(kScoredThreads) void k_route_scored(ScoredArgs a) {
     }
 }
 
+// ------------------------------------------------------------------ chunks
+
+namespace {
+
+constexpr int kPast = 0x7FFFFF00;    // byte offset past every descriptor's end
+
+// How k_route_chunks lays a row out; lanes == 0: the shape is not for it.
+struct ChunkPlan {
+    int lanes;   // per token
+    int rows;    // chunks per lane
+    int cg_lg;   // slots per group: 1 << cg_lg, the last ones empty
+    int wide;    // chunks are whole and aligned for one load each
+};
+
+// The two largest of a1 >= a2 and the partner's pair b1 >= b2.
+__device__ __forceinline__ void two_best(float& a1, float& a2, float b1, float b2) {
+    const float lo = fminf(a1, b1);
+    a1 = fmaxf(a1, b1);
+    a2 = fmaxf(lo, fmaxf(a2, b2));
+}
+
+// The value of the lane across from this one in a butterfly of 2 D lanes; for
+// D >= 4 any lane of the other half (they hold the same by then).
+template <int D>
+__device__ __forceinline__ float across(float v) {
+    if constexpr (D == 1) return dpp_f32<kDppQuadXor1>(v);
+    else if constexpr (D == 2) return dpp_f32<kDppQuadXor2>(v);
+    else if constexpr (D == 4) return dpp_f32<kDppRowHalfMirror>(v);
+    else if constexpr (D == 8) return dpp_f32<kDppRowMirror>(v);
+    else return __shfl_xor(v, D, kWave);
+}
+
+}  // namespace
+
+// S lanes per token, R chunks of four experts per lane: slot g + S i is row i of
+// lane g. A group of experts has 1 << cg_lg slots (without groups the whole row
+// is one), so its slots are neighbouring lanes, or whole rows, and its two best
+// keys are a butterfly over them. Slots ascend with the experts, so a tie goes
+// to the lower position 4 slot + x.
+//
+// A round is the best key of a lane, the maximum over the token's lanes (DPP,
+// permlane swaps), and the position of its holder: by ballot and readlane where
+// a wave holds one token and the maximum is unique, else a minimum over the
+// lanes. Lane r keeps the winner of round r.
+//
+// Bound by instructions, about half of them the fp64 scores and half the group
+// choice and the rounds: 16384 tokens, 256 experts in 8 groups, k 8, sigmoid
+// with bias 16.9 us (1.0 TB/s; the first kernel, one token per wave with the
+// device library's exp and a serial group scan, took 29.9 us); one token 4.2 us
+// (7.3 us). Tried: sorting networks over packed (key, expert) doubles with 8
+// lanes per token, 19.2 us and 13.0 us; every lane then works through 32
+// experts in series, and few waves hide it.
+template <int S, int R, bool SIGMOID, bool GROUPED>
+__global__ __launch_bounds__(kScoredThreads) void k_route_chunks(ScoredArgs a, ChunkPlan p) {
+    __shared__ float4 s_score[R][kScoredThreads];        // [row][lane of every token]
+    __shared__ uint32_t s_group[GROUPED ? kScoredThreads * R : 1];
+    constexpr int kTokens = kScoredThreads / S;
+    const int tid = threadIdx.x, g = tid & (S - 1), tl = tid / S;
+    const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+    const int64_t t = t0 + tl;
+    const bool live = t < a.T;
+    const int E = a.E, k = a.k, ks = a.k + a.n_shared;
+    const int per = GROUPED ? E / a.n_group : E;
+    const int cg_mask = (1 << p.cg_lg) - 1;
+    const int size = a.bf16 ? 2 : 4;
+
+    // this block's rows of logits, bounded by the last one's end
+    const int64_t left = a.T - t0;
+    const int64_t block_rows = left < kTokens ? left : kTokens;
+    const auto rs = range_rsrc(static_cast<const char*>(a.logits) + t0 * a.ld * size,
+                               (int)(((block_rows - 1) * a.ld + E) * size));
+    const int row_off = live ? (int)(tl * a.ld) * size : kPast;
+    int e0[R], n[R];                                     // first expert, experts held
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+        const int slot = g + S * i;
+        const int group = GROUPED ? slot >> p.cg_lg : 0;
+        const int in = GROUPED ? slot & cg_mask : slot;
+        e0[i] = group * per + 4 * in;
+        n[i] = !GROUPED || group < a.n_group ? per - 4 * in : 0;
+    }
+    float l[R][4];
+    if (p.wide && a.bf16) {
+        uint32_t u[R][2];
+#pragma unroll
+        for (int i = 0; i < R; i++) {
+            const auto h = __builtin_amdgcn_raw_buffer_load_b64(
+                rs, live && n[i] > 0 ? row_off + e0[i] * 2 : kPast, 0, 0);
+            u[i][0] = h[0];
+            u[i][1] = h[1];
+        }
+#pragma unroll
+        for (int i = 0; i < R; i++) {
+            l[i][0] = bf16_lo(u[i][0]);
+            l[i][1] = bf16_hi(u[i][0]);
+            l[i][2] = bf16_lo(u[i][1]);
+            l[i][3] = bf16_hi(u[i][1]);
+        }
+    } else if (p.wide) {
+        u32x4 u[R];
+#pragma unroll
+        for (int i = 0; i < R; i++)
+            u[i] = __builtin_amdgcn_raw_buffer_load_b128(
+                rs, live && n[i] > 0 ? row_off + e0[i] * 4 : kPast, 0, 0);
+#pragma unroll
+        for (int i = 0; i < R; i++)
+#pragma unroll
+            for (int x = 0; x < 4; x++) l[i][x] = __uint_as_float(u[i][x]);
+    } else if (a.bf16) {
+#pragma unroll
+        for (int i = 0; i < R; i++)
+#pragma unroll
+            for (int x = 0; x < 4; x++)
+                l[i][x] = bf16_lo((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                    rs, live && x < n[i] ? row_off + (e0[i] + x) * 2 : kPast, 0, 0));
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; i++)
+#pragma unroll
+            for (int x = 0; x < 4; x++)
+                l[i][x] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                    rs, live && x < n[i] ? row_off + (e0[i] + x) * 4 : kPast, 0, 0));
+    }
+    const auto rb = range_rsrc(a.bias, a.bias ? E * 4 : 0);   // no bias: zeros
+    float b[R][4];
+#pragma unroll
+    for (int i = 0; i < R; i++)
+#pragma unroll
+        for (int x = 0; x < 4; x++)
+            b[i][x] = __uint_as_float(
+                __builtin_amdgcn_raw_buffer_load_b32(rb, (e0[i] + x) * 4, 0, 0));
+
+    // scores; masked logits (-inf, NaN) and empty places as -inf
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < R; i++)
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+            // +inf: the largest finite value in the softmax
+            if (!SIGMOID) l[i][x] = l[i][x] > 3.402823466e38f ? 3.402823466e38f : l[i][x];
+            l[i][x] = (x < n[i]) & (l[i][x] > -INFINITY) ? l[i][x] : -INFINITY;
+            m = fmaxf(m, l[i][x]);
+        }
+    float s[R][4];
+    if constexpr (SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < R; i++)
+#pragma unroll
+            for (int x = 0; x < 4; x++) s[i][x] = sigmoid32(l[i][x]);
+    } else {
+        m = __uint_as_float(group_reduce<S>(__float_as_uint(m), FMax()));
+        double pr[R][4], sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < R; i++)
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+                pr[i][x] = exp_diff(l[i][x], m);         // a masked one: exp(-150), nothing
+                sum += pr[i][x];
+            }
+#pragma unroll
+        for (int d = 1; d < S; d <<= 1) sum += __shfl_xor(sum, d, kWave);
+        const double inv = recip64(sum);
+#pragma unroll
+        for (int i = 0; i < R; i++)
+#pragma unroll
+            for (int x = 0; x < 4; x++) s[i][x] = (float)(pr[i][x] * inv);
+    }
+    uint32_t c[R][4];                                    // choice keys, 0: never chosen
+    float key[R][4];
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+        s_score[i][tid] = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+            key[i][x] = s[i][x] + b[i][x];
+            key[i][x] = (l[i][x] > -INFINITY) & (key[i][x] > -INFINITY) ? key[i][x] : -INFINITY;
+            c[i][x] = key[i][x] > -INFINITY ? order_key(key[i][x]) : 0u;
+        }
+    }
+
+    if constexpr (GROUPED) {
+        float t1[R], t2[R];
+#pragma unroll
+        for (int i = 0; i < R; i++) {
+            t1[i] = fmaxf(key[i][0], key[i][1]);
+            t2[i] = fminf(key[i][0], key[i][1]);
+            two_best(t1[i], t2[i], fmaxf(key[i][2], key[i][3]), fminf(key[i][2], key[i][3]));
+            if (p.cg_lg > 0) two_best(t1[i], t2[i], across<1>(t1[i]), across<1>(t2[i]));
+            if (p.cg_lg > 1) two_best(t1[i], t2[i], across<2>(t1[i]), across<2>(t2[i]));
+            if (p.cg_lg > 2) two_best(t1[i], t2[i], across<4>(t1[i]), across<4>(t2[i]));
+            if (S > 8 && p.cg_lg > 3) two_best(t1[i], t2[i], across<8>(t1[i]), across<8>(t2[i]));
+            if (S > 16 && p.cg_lg > 4) two_best(t1[i], t2[i], across<16>(t1[i]), across<16>(t2[i]));
+            if (S > 32 && p.cg_lg > 5) two_best(t1[i], t2[i], across<32>(t1[i]), across<32>(t2[i]));
+        }
+        // groups of two or four whole rows
+        const int spans = (1 << p.cg_lg) / S;
+        if (R > 1 && spans >= 2) {
+#pragma unroll
+            for (int i = 0; i + 1 < R; i += 2) {
+                two_best(t1[i], t2[i], t1[i + 1], t2[i + 1]);
+                t1[i + 1] = t1[i];
+                t2[i + 1] = t2[i];
+            }
+        }
+        if (R > 2 && spans >= 4) {
+#pragma unroll
+            for (int i = 0; i + 3 < R; i += 4) {
+                two_best(t1[i], t2[i], t1[i + 2], t2[i + 2]);
+                t1[i + 1] = t1[i + 2] = t1[i + 3] = t1[i];
+                t2[i + 1] = t2[i + 2] = t2[i + 3] = t2[i];
+            }
+        }
+        uint32_t gk[R];
+        uint32_t* const mine = s_group + tl * (S * R);
+#pragma unroll
+        for (int i = 0; i < R; i++) {
+            const int slot = g + S * i;
+            gk[i] = t1[i] > -INFINITY
+                ? order_key(a.group_top == 2 && t2[i] > -INFINITY ? t1[i] + t2[i] : t1[i]) : 0u;
+            if ((slot & cg_mask) == 0) mine[slot >> p.cg_lg] = gk[i];
+        }
+        __syncthreads();
+        int before[R];                                   // groups that rank before this one
+#pragma unroll
+        for (int i = 0; i < R; i++) before[i] = 0;
+#pragma unroll 4
+        for (int o = 0; o < a.n_group; o++) {
+            const uint32_t v = mine[o];
+#pragma unroll
+            for (int i = 0; i < R; i++)
+                before[i] += (v > gk[i]) | ((v == gk[i]) & (o < ((g + S * i) >> p.cg_lg))) ? 1 : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < R; i++)
+#pragma unroll
+            for (int x = 0; x < 4; x++) c[i][x] = before[i] < a.topk_group ? c[i][x] : 0u;
+    }
+
+    uint32_t sel_key = 0u, sel_pos = 0u;
+    for (int r = 0; r < k; r++) {
+        uint32_t best = 0u;
+#pragma unroll
+        for (int i = 0; i < R; i++)
+#pragma unroll
+            for (int x = 0; x < 4; x++) best = best > c[i][x] ? best : c[i][x];
+        const uint32_t top = group_reduce<S>(best, UMax());
+        uint32_t pos = 0xFFFFFFFFu;                      // this lane's lowest holder
+#pragma unroll
+        for (int i = R - 1; i >= 0; i--)
+#pragma unroll
+            for (int x = 3; x >= 0; x--) pos = c[i][x] == top ? 4u * (g + S * i) + x : pos;
+        if constexpr (S == kWave) {
+            const uint64_t mask = __ballot(best == top);
+            if (__popcll(mask) == 1)
+                pos = (uint32_t)__builtin_amdgcn_readlane((int)pos, (int)__builtin_ctzll(mask));
+            else
+                pos = group_reduce<S>(pos, UMin());
+        } else {
+            pos = group_reduce<S>(pos, UMin());
+        }
+#pragma unroll
+        for (int i = 0; i < R; i++)
+#pragma unroll
+            for (int x = 0; x < 4; x++) c[i][x] = pos == 4u * (g + S * i) + x ? 0u : c[i][x];
+        sel_key = g == r ? top : sel_key;
+        sel_pos = g == r ? pos : sel_pos;
+    }
+
+    // weights: lane r has slot r
+    __syncthreads();
+    const bool mine = g < k && sel_key != 0u;
+    const int slot = (int)(sel_pos >> 2);
+    const float* const row = reinterpret_cast<const float*>(
+        &s_score[mine ? slot / S : 0][tl * S + (mine ? slot & (S - 1) : 0)]);
+    float w = mine ? row[sel_pos & 3] : 0.0f;
+    const float total = __uint_as_float(group_reduce<S>(__float_as_uint(w), FAdd()));
+    if (!live) return;
+    if (g < k) {
+        const int e = (GROUPED ? (slot >> p.cg_lg) * per + 4 * (slot & cg_mask) : 4 * slot) +
+                      (int)(sel_pos & 3);
+        if (a.renorm) w = total > 0.0f ? w / total : 0.0f;
+        a.topk_idx[t * ks + g] = mine ? e : -1;
+        a.topk_w[t * ks + g] = w * a.scale;
+    }
+    for (int sh = g; sh < a.n_shared; sh += S) {
+        a.topk_idx[t * ks + k + sh] = E + sh;
+        a.topk_w[t * ks + k + sh] = a.shared_w;
+    }
+}
+
+namespace {
+
+ChunkPlan chunk_plan(const ScoredArgs& a) {
+    ChunkPlan p{0, 1, 0, 0};
+    const bool grouped = a.topk_group < a.n_group;
+    const int per = grouped ? a.E / a.n_group : a.E;
+    while (4 << p.cg_lg < per) p.cg_lg++;
+    const int slots = grouped ? a.n_group << p.cg_lg : (per + 3) / 4;
+    // a block's rows have to fit a buffer descriptor
+    if (slots > 4 * kWave || a.k > kWave || a.ld > (1 << 20)) return p;
+    // One chunk per lane is quickest for one token; where many tokens share the
+    // chip, half the lanes with twice the chunks save instructions: 16384 tokens
+    // of 256 experts, 19.0 -> 16.9 us (sigmoid, 8 groups), 17.3 -> 14.4 us
+    // (softmax, no groups); a quarter of the lanes: 16.5 and 13.4 us there, but
+    // 6.4 -> 7.8 us with 4096 tokens of 160 experts.
+    int lanes = 8;
+    while (lanes < kWave && (lanes < slots || lanes < a.k)) lanes <<= 1;
+    if (a.T >= 2048 && lanes > 8 && lanes / 2 >= a.k && slots <= lanes * 2) lanes >>= 1;
+    while (p.rows * lanes < slots) p.rows <<= 1;
+    p.lanes = lanes;
+    const uintptr_t base = reinterpret_cast<uintptr_t>(a.logits);
+    p.wide = per % 4 == 0 && (!a.bf16 || (a.ld % 2 == 0 && base % 4 == 0));
+    return p;
+}
+
+template <int S, int R>
+void launch_chunks(const ScoredArgs& a, const ChunkPlan& p, int64_t blocks, hipStream_t stream) {
+    const dim3 grid((unsigned)blocks), block(kScoredThreads);
+    const bool grouped = a.topk_group < a.n_group;
+    if (a.sigmoid && grouped) k_route_chunks<S, R, true, true><<<grid, block, 0, stream>>>(a, p);
+    else if (a.sigmoid) k_route_chunks<S, R, true, false><<<grid, block, 0, stream>>>(a, p);
+    else if (grouped) k_route_chunks<S, R, false, true><<<grid, block, 0, stream>>>(a, p);
+    else k_route_chunks<S, R, false, false><<<grid, block, 0, stream>>>(a, p);
+}
+
+}  // namespace
+
 hipError_t launch_route_scored(const ScoredArgs& a, hipStream_t stream, LaunchInfo* info,
                                bool run) {
+    const ChunkPlan p = chunk_plan(a);
+    if (p.lanes) {
+        const int64_t per_block = kScoredThreads / p.lanes;
+        const int64_t blocks = (a.T + per_block - 1) / per_block;
+        if (info) *info = LaunchInfo{blocks, kScoredThreads, 0, p.lanes, "route_chunks"};
+        if (!run || blocks == 0) return hipSuccess;
+        switch (p.lanes * 8 + p.rows) {
+            case 8 * 8 + 1: launch_chunks<8, 1>(a, p, blocks, stream); break;
+            case 16 * 8 + 1: launch_chunks<16, 1>(a, p, blocks, stream); break;
+            case 32 * 8 + 1: launch_chunks<32, 1>(a, p, blocks, stream); break;
+            case 8 * 8 + 2: launch_chunks<8, 2>(a, p, blocks, stream); break;
+            case 16 * 8 + 2: launch_chunks<16, 2>(a, p, blocks, stream); break;
+            case 32 * 8 + 2: launch_chunks<32, 2>(a, p, blocks, stream); break;
+            case 32 * 8 + 4: launch_chunks<32, 4>(a, p, blocks, stream); break;
+            case 64 * 8 + 1: launch_chunks<64, 1>(a, p, blocks, stream); break;
+            case 64 * 8 + 2: launch_chunks<64, 2>(a, p, blocks, stream); break;
+            default: launch_chunks<64, 4>(a, p, blocks, stream);
+        }
+        return hipGetLastError();
+    }
     const int nv = (a.E + kWave - 1) / kWave;
     const int64_t blocks = (a.T + kScoredWaves - 1) / kScoredWaves;
     const size_t lds = (size_t)kScoredWaves * (2 * a.E + a.k + a.n_group) * 4;
-    if (info) *info = LaunchInfo{blocks, kScoredThreads, lds, nv, "route_scored"};
+    if (info) *info = LaunchInfo{blocks, kScoredThreads, lds, nv, "route_rounds"};
     if (!run || blocks == 0) return hipSuccess;
     const dim3 grid((unsigned)blocks), block(kScoredThreads);
-    if (nv <= 1) k_route_scored<1><<<grid, block, lds, stream>>>(a);
-    else if (nv <= 2) k_route_scored<2><<<grid, block, lds, stream>>>(a);
-    else if (nv <= 4) k_route_scored<4><<<grid, block, lds, stream>>>(a);
-    else if (nv <= 8) k_route_scored<8><<<grid, block, lds, stream>>>(a);
-    else k_route_scored<16><<<grid, block, lds, stream>>>(a);
+    if (nv <= 1) k_route_rounds<1><<<grid, block, lds, stream>>>(a);
+    else if (nv <= 2) k_route_rounds<2><<<grid, block, lds, stream>>>(a);
+    else if (nv <= 4) k_route_rounds<4><<<grid, block, lds, stream>>>(a);
+    else if (nv <= 8) k_route_rounds<8><<<grid, block, lds, stream>>>(a);
+    else k_route_rounds<16><<<grid, block, lds, stream>>>(a);
     return hipGetLastError();
 }
 
