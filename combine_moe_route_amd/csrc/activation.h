@@ -8,13 +8,34 @@ namespace moe {
 
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
 
+// z Phi(z), Phi the normal distribution: for z < 0 it is z h, else z (1 - h), with
+// h = erfc(x) / 2, x = |z| / sqrt 2. erfc(x) = t Q(t) exp(-x^2), t = 1 / (1 + 0.3 x),
+// where Q is the polynomial of degree 8 whose largest relative error over
+// 0 <= x <= 12 is least (2.1e-8, fitted to exp(x^2) erfc(x) / t). In fp32 the
+// result is within 2^-21 |z|, and relatively within 2e-6 down to z = -8. The
+// device library's erfc took four times the instructions: with it the gated
+// activation of 6185 rows of 1408 channels was bound by them.
+__device__ __forceinline__ float gelu(float z) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.21213203435596426f, fabsf(z), 1.0f));
+    float q = -0.129252457f;
+    q = fmaf(q, t, 0.484298284f);
+    q = fmaf(q, t, -0.509765798f);
+    q = fmaf(q, t, 0.544960012f);
+    q = fmaf(q, t, -0.0928216458f);
+    q = fmaf(q, t, 0.214179706f);
+    q = fmaf(q, t, 0.148521657f);
+    q = fmaf(q, t, 0.170690877f);
+    q = fmaf(q, t, 0.169189357f);
+    const float h = 0.5f * t * q * __expf(-0.5f * z * z);
+    return z < 0.0f ? z * h : fmaf(-z, h, z);
+}
+
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
     if constexpr (ACT == kActRelu) return z < 0.0f ? 0.0f : z;      // NaN stays NaN
     // z * sigmoid(z): exp(-z) overflows to inf for very negative z, giving -0
     if constexpr (ACT == kActSilu) return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
-    // erfc keeps the relative precision of the negative tail, 1 + erf does not
-    if constexpr (ACT == kActGelu) return 0.5f * z * erfcf(z * -0.70710678118654752f);
+    if constexpr (ACT == kActGelu) return gelu(z);
     return z;
 }
 
