@@ -131,7 +131,7 @@ def _run(name: str, dev: torch.device, *args):
     """lib.<name>(*args, stream) on torch's current stream of `dev`, with that
     device current; a non-zero status raises. Tensors go as addresses."""
     fn = getattr(lib, name)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
@@ -145,6 +145,9 @@ def _addr(t: Optional[torch.Tensor]):
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape=None, device=None):
+    if (t.dtype is dtype and t.is_cuda and (device is None or t.device == device)
+            and t.is_contiguous() and (shape is None or t.shape == shape)):
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_cuda:

@@ -97,7 +97,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ off, int E
         if (e < E) {
             r0[i] = min(max(off[e], 0), max_rows);
             r1[i] = min(max(off[e + 1], 0), max_rows);
-            n[i] = r1[i] > r0[i] ? (r1[i] - r0[i] + BM - 1) / BM : 0;
+            n[i] = r1[i] > r0[i] ? (r1[i] - r0[i] - 1) / BM + 1 : 0;
         }
         sum += n[i];
     }
@@ -108,6 +108,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ off, int E
         if (lane >= d) incl += v;
     }
     if (lane == 63) s_wave[wave] = incl;
+    if (tid == 0) s_tile[0] = s_tile[1] = s_tile[2] = s_tile[3] = 0;
     __syncthreads();
     int before = 0, total = 0;
 #pragma unroll
@@ -141,8 +142,10 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ off, int E
     out.rows = __builtin_amdgcn_readfirstlane(s_tile[1]);
     out.e = __builtin_amdgcn_readfirstlane(s_tile[2]);
     nt_out = __builtin_amdgcn_readfirstlane(s_tile[3]);
+    // offsets that do not ascend can name no tile, or more than one
+    out.rows = min(out.rows, max_rows - out.row0);
     __syncthreads();                                     // the scratch is free again
-    return true;
+    return out.rows > 0;
 }
 
 // Eight bf16 values at p (16-byte aligned) to fp32.
@@ -639,36 +642,47 @@ hipError_t launch_shape(const GemmBf16Args& g, hipStream_t stream, LaunchInfo* i
 
 }  // namespace
 
-// The shape of a call, from what the host knows: rows per expert that can have
-// any, r, and the number of tiles of each shape.
+// The shape of a call, from what the host knows: the capacity, from which the
+// rows of an expert that has any, r (with padded segments more than there are).
 //
-// r <= 32: every weight is read once and nothing else counts. Skinny tiles
-// with streamed weights: 128 tokens over 256 experts, K 7168, N 4096 (gated):
-// 2000 us (7.4 TB/s), 2261 us without the hint, 2300 us with Medium tiles.
+// r <= 32: every weight is read about once and nothing else counts: Skinny.
+// With rows of whole 128-byte lines (K % 64 == 0) the weights are streamed: 128
+// tokens over 256 experts, K 7168, N 4096 (gated): 2000 us (7.4 TB/s), 2261 us
+// without the hint, 2300 us with Medium tiles. Lines shared by two k-blocks
+// would be fetched twice (18 tokens, K 2200: 49 us streamed, 38 us not).
 //
-// Otherwise the shape with the least estimated time: full rounds of the
-// chip times a round's time, in units of a round of Large tiles (two
-// workgroups on a CU share its time; a lone Small tile takes 0.5). Measured
-// (us) for E x rows, N, K:          Large  Medium  Small  Skinny
-//   16 x 400, 4096, 2048              121     133    148     383
-//    8 x 1000, 4096, 4096             219     265    290     834
-//   32 x 600, 1024, 1024               57      54     53     173
-//    1 x 2048, 4096, 4096              84      65     66     199
-//   12 x 194, 1032, 1016               27      20     16      29
-//    1 x 128, 4096, 4096               70      41     35      20
+// Otherwise the shape of least estimated time: rounds of the chip times the
+// time of a round, start + k-blocks times a rate (us), fitted to:
+//   us, experts x rows, N, K           Large  Medium  Small  Skinny
+//   16 x 400, 4096, 2048                121     133    148     383
+//    8 x 1000, 4096, 4096               219     265    290     834
+//   55 x 286, 2336, 392                 123      95     85     233
+//   37 x 480, 2352, 144                  73      57     54     230
+//    1 x 2048, 4096, 4096                84      65     66     199
+//   12 x 194, 1032, 1016                 27      20     16      29
+//    1 x 128, 4096, 4096                 70      41     35      20
+//    5 x 217, 416, 4584                  84      66     46      23
+// A segment ends inside a tile, half a tile on average; a lone segment's tiles
+// are known. The last round counts a quarter more than its share.
 hipError_t launch_grouped_gemm_bf16(const GemmBf16Args& g, hipStream_t stream, LaunchInfo* info,
                                     bool run) {
     const int64_t hit = g.E < g.max_rows ? g.E : g.max_rows;
-    const int64_t r = hit ? (g.max_rows + hit - 1) / hit : 0;
-    if (r <= 32) return launch_shape<Skinny<true>>(g, stream, info, run);
-    auto rounds = [&](int bm, int bn, int slots, double time) {
-        const int64_t tiles = hit * ((r + bm - 1) / bm) * ((g.N + bn - 1) / bn);
-        return (double)((tiles + slots - 1) / slots) * time;
+    const double r = hit ? (double)g.max_rows / hit : 0.0;
+    if (r <= 32.0)
+        return g.K % 64 == 0 ? launch_shape<Skinny<true>>(g, stream, info, run)
+                             : launch_shape<Skinny<false>>(g, stream, info, run);
+    const double kb = (g.K + kBK - 1) / kBK;
+    auto items = [&](int bm, int bn) {
+        double per = r / bm + 0.5;
+        if (hit == 1) per = (double)((g.max_rows + bm - 1) / bm);
+        return hit * (per > 1.0 ? per : 1.0) * ((g.N + bn - 1) / bn);
     };
-    const double large = rounds(256, 256, 256, 1.0), medium = rounds(128, 256, 256, 0.67);
-    const double lone = rounds(128, 128, 256, 0.5), pair = rounds(128, 128, 512, 0.72);
-    const double small = lone <= 0.5 ? lone : pair;
-    const double skinny = rounds(32, 64, 512, 0.38);
+    auto rounds = [](double n, int slots) { return n <= slots ? 1.0 : n / slots + 0.25; };
+    const double small_n = items(128, 128), skinny_n = items(32, 64);
+    const double large = rounds(items(256, 256), 256) * (12.0 + 1.6 * kb);
+    const double medium = rounds(items(128, 256), 256) * (8.0 + 1.0 * kb);
+    const double small = small_n <= 256 ? 5.0 + 0.55 * kb : rounds(small_n, 512) * (6.0 + 1.1 * kb);
+    const double skinny = skinny_n <= 256 ? 2.0 + 0.23 * kb : rounds(skinny_n, 512) * (3.0 + 0.4 * kb);
     if (large <= medium && large <= small && large <= skinny)
         return launch_shape<Large>(g, stream, info, run);
     if (medium <= small && medium <= skinny) return launch_shape<Medium>(g, stream, info, run);
