@@ -242,3 +242,53 @@ def test_python_refusals():
         moe_grouped_gemm_bf16(a[:, :60].contiguous(), off, w[:, :, :60].contiguous())
     with pytest.raises(MoeRouteError):
         moe_grouped_gemm_bf16(a, off, w[:, :24].contiguous(), gated=True)
+
+
+def test_rows_past_32_bit_offsets():
+    """A segment whose rows of a, residual and y start beyond 2^32 bytes."""
+    log("large rows")
+    R, K, N = 600_000, 4096, 4096
+    a = torch.zeros((R, K), dtype=torch.bfloat16, device=DEV)
+    y = torch.full((R, N), SENTINEL, dtype=torch.int16, device=DEV).view(torch.bfloat16)
+    first, gen = R - 300, torch.Generator(DEV).manual_seed(3)
+    a[first:] = torch.randn((300, K), device=DEV, generator=gen).to(torch.bfloat16)
+    w = (torch.randn((2, N, K), device=DEV, generator=gen) / 64).to(torch.bfloat16)
+    from combine_moe_route_amd import moe_grouped_gemm_bf16
+    for segs in ([first, first + 20, R], [first, R, R], [R - 9, R, R]):
+        y.view(torch.int16).fill_(SENTINEL)
+        moe_grouped_gemm_bf16(a, torch.tensor(segs, dtype=torch.int32, device=DEV), w, y=y)
+        torch.cuda.synchronize()
+        base = segs[0]
+        ref = reference(a[base:], [s - base for s in segs], w[:, :64].contiguous(), None, "none",
+                        False, None)
+        for (r0, r1), (want, tol) in ref.items():
+            assert ((y[base + r0:base + r1, :64].double().cpu() - want).abs() <= tol).all()
+        assert (y[base - 1].view(torch.int16) == SENTINEL).all()
+        assert (y[0].view(torch.int16) == SENTINEL).all()
+
+
+def test_tile_shapes_of_the_rule():
+    """Each tile shape is reached, by the launch log (MOE_ROUTE_LOG=1), and gives
+    the reference's result; read in a child process."""
+    import os
+    import re
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    cases = [  # counts, K, N, gated -> (rows of a tile, threads)
+        (([20, 3], 128, 128, False), ("32", "256")),          # streamed weights
+        (([20, 3], 136, 128, True), ("32", "256")),           # not whole lines
+        (([97, 90, 80], 4168, 744, False), ("32", "256")),    # few tiles, deep
+        (([120] * 12, 1016, 1032, False), ("128", "256")),
+        (([2048], 2048, 4096, False), ("128", "512")),
+        (([1000] * 8, 2048, 4096, True), ("256", "256")),
+    ]
+    code = ("import sys; sys.path.insert(0, 'tests')\n"
+            "from test_gpu_gemm_bf16 import case, check\n"
+            f"for c, K, N, g in {[c for c, _ in cases]!r}:\n"
+            "    check(case(c, K, N, gated=g), 'silu')\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=110, env=dict(os.environ, MOE_ROUTE_LOG="1"))
+    assert r.returncode == 0, r.stderr[-2000:]
+    got = re.findall(r"grouped_gemm_bf16 grid=\d+ block=(\d+) lds=\d+ param=(\d+)", r.stderr)
+    assert [(p, b) for b, p in got] == [want for _, want in cases]
