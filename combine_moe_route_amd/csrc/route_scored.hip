@@ -413,22 +413,13 @@ __global__ __launch_bounds__(kScoredThreads) void k_route_chunks(ScoredArgs a, C
             if (S > 16 && p.cg_lg > 4) two_best(t1[i], t2[i], across<16>(t1[i]), across<16>(t2[i]));
             if (S > 32 && p.cg_lg > 5) two_best(t1[i], t2[i], across<32>(t1[i]), across<32>(t2[i]));
         }
-        // groups of two or four whole rows
-        const int spans = (1 << p.cg_lg) / S;
-        if (R > 1 && spans >= 2) {
+        // a group of more slots than lanes is two rows (there are at most four)
+        if (R > 2 && 1 << p.cg_lg > S) {
 #pragma unroll
             for (int i = 0; i + 1 < R; i += 2) {
                 two_best(t1[i], t2[i], t1[i + 1], t2[i + 1]);
                 t1[i + 1] = t1[i];
                 t2[i + 1] = t2[i];
-            }
-        }
-        if (R > 2 && spans >= 4) {
-#pragma unroll
-            for (int i = 0; i + 3 < R; i += 4) {
-                two_best(t1[i], t2[i], t1[i + 2], t2[i + 2]);
-                t1[i + 1] = t1[i + 2] = t1[i + 3] = t1[i];
-                t2[i + 1] = t2[i + 2] = t2[i + 3] = t2[i];
             }
         }
         uint32_t gk[R];

@@ -196,6 +196,30 @@ def test_shared_slots_and_given_outputs():
     assert e[0].shape == (0, k)
 
 
+@pytest.mark.parametrize("T,E,k,G,KG,top", [
+    (9, 1024, 8, 1024, 100, 1), (7, 1000, 5, 500, 50, 2), (6, 1023, 9, 3, 2, 2), (4, 1024, 70, 2, 1, 2),
+    (2100, 512, 8, 2, 1, 2), (2100, 1024, 4, 2, 1, 2), (2050, 40, 20, 5, 4, 1), (2048, 250, 8, 1, 1, 2),
+    (3, 1024, 64, 1, 1, 2), (5, 1021, 33, 1, 1, 2), (2100, 12, 9, 2, 1, 2), (2060, 257, 12, 1, 1, 1),
+])
+def test_many_groups_wide_groups_and_both_kernels(T, E, k, G, KG, top):
+    """Groups of one expert, groups wider than the lanes, odd widths, k past the
+    lanes; batches on either side of the switch to fewer lanes per token."""
+    if k > KG * (E // G):
+        k = KG * (E // G)
+    log(f"groups T={T} E={E} k={k} G={G}/{KG}")
+    rows = min(T, 40)
+    from combine_moe_route_amd import moe_route_scored
+    for score, dtype in (("sigmoid", torch.float32), ("softmax", torch.bfloat16)):
+        l = logits_of(T, E, 20, dtype, masked=0.1)
+        kw = dict(score=score, n_group=G, topk_group=KG, group_top=top)
+        idx, w = moe_route_scored(l, k, bias=torch.tensor(bias_of(E, 21), device=DEV), **kw)
+        pick = torch.linspace(0, T - 1, rows).long()
+        ri, rw, total = plain(l[pick.to(DEV)].double().cpu().numpy(), k, bias=bias_of(E, 21), **kw)
+        assert np.array_equal(idx.cpu().numpy()[pick], ri)
+        err = np.abs(w.double().cpu().numpy()[pick] - rw)
+        assert np.all(err <= (k + 4) * 2.0 ** -24 * np.abs(rw) + 2.0 ** -149)
+
+
 def test_large_batch_strided_and_row_sample():
     """A prefill batch whose row offsets pass 2^31 bytes; rows sampled."""
     log("large strided")
