@@ -19,6 +19,7 @@
 // lanes per token, k_route_rounds for every other shape.
 #include "launch.h"
 #include "moe_device.h"
+#include "topk_sort.h"
 
 namespace moe {
 
@@ -84,6 +85,12 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
     return v;
+}
+
+// Candidate of an order key and a position below 1024, as in topk_sort.h.
+__device__ __forceinline__ double key_pack(uint32_t key, int pos) {
+    return __hiloint2double((int)__builtin_amdgcn_alignbit(0x400u, key, 12),
+                            (int)((key << 20) | (uint32_t)(1023 - pos)));
 }
 
 // Order key of a selection value; 0 for one that can never be chosen.
@@ -229,9 +236,35 @@ constexpr int kPast = 0x7FFFFF00;    // byte offset past every descriptor's end
 struct ChunkPlan {
     int lanes;   // per token
     int rows;    // chunks per lane
+    int sorted;  // sorting networks instead of rounds (rows == 4, k <= kList)
     int cg_lg;   // slots per group: 1 << cg_lg, the last ones empty
     int wide;    // chunks are whole and aligned for one load each
 };
+
+constexpr int kList = 8;             // candidates the sorting networks keep
+
+// The list of the 2 D lanes a butterfly step joins; across rows of 16 lanes both
+// rows' lists come from one swap.
+template <int D>
+__device__ __forceinline__ void join_lists(double (&list)[kList]) {
+    if constexpr (D < 16) {
+        merge_with_partner<D, kList>(list);
+    } else {
+        double other[kList];
+#pragma unroll
+        for (int q = 0; q < kList; q++) {
+            const uint32_t hi = (uint32_t)__double2hiint(list[q]);
+            const uint32_t lo = (uint32_t)__double2loint(list[q]);
+            const auto h = D == 16 ? __builtin_amdgcn_permlane16_swap(hi, hi, false, false)
+                                   : __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+            const auto l = D == 16 ? __builtin_amdgcn_permlane16_swap(lo, lo, false, false)
+                                   : __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+            list[q] = __hiloint2double((int)h[0], (int)l[0]);
+            other[q] = __hiloint2double((int)h[1], (int)l[1]);
+        }
+        merge_top<kList>(list, other);
+    }
+}
 
 // The two largest of a1 >= a2 and the partner's pair b1 >= b2.
 __device__ __forceinline__ void two_best(float& a1, float& a2, float b1, float b2) {
@@ -259,19 +292,21 @@ __device__ __forceinline__ float across(float v) {
 // keys are a butterfly over them. Slots ascend with the experts, so a tie goes
 // to the lower position 4 slot + x.
 //
-// A round is the best key of a lane, the maximum over the token's lanes (DPP,
-// permlane swaps), and the position of its holder: by ballot and readlane where
-// a wave holds one token and the maximum is unique, else a minimum over the
-// lanes. Lane r keeps the winner of round r.
+// The k best, SORTED: a lane sorts its 16 candidates, packed with their positions
+// into doubles as in topk_sort.h, down to a list of 8, and the lists of the
+// token's lanes are merged by a butterfly. Otherwise in k rounds: the best key
+// of a lane, the maximum over the token's lanes (DPP, permlane swaps), and the
+// position of its holder, by ballot and readlane where a wave holds one token
+// and the maximum is unique, else a minimum over the lanes. Lane r keeps the
+// winner of round r.
 //
-// Bound by instructions, about half of them the fp64 scores and half the group
-// choice and the rounds: 16384 tokens, 256 experts in 8 groups, k 8, sigmoid
-// with bias 16.9 us (1.0 TB/s; the first kernel, one token per wave with the
-// device library's exp and a serial group scan, took 29.9 us); one token 4.2 us
-// (7.3 us). Tried: sorting networks over packed (key, expert) doubles with 8
-// lanes per token, 19.2 us and 13.0 us; every lane then works through 32
-// experts in series, and few waves hide it.
-template <int S, int R, bool SIGMOID, bool GROUPED>
+// Bound by instructions, about half of them the fp64 scores: 16384 tokens, 256
+// experts in 8 groups, k 8, sigmoid with bias 14.5 us (1.2 TB/s; the first
+// kernel, one token per wave with the device library's exp and a serial group
+// scan, took 29.9 us); one token 4.1 us (7.3 us). Tried: sorting with 8 lanes
+// per token and keys waiting in LDS, 19.2 us and 13.0 us; every lane then works
+// through 32 experts in series.
+template <int S, int R, bool SORTED, bool SIGMOID, bool GROUPED>
 __global__ __launch_bounds__(kScoredThreads) void k_route_chunks(ScoredArgs a, ChunkPlan p) {
     __shared__ float4 s_score[R][kScoredThreads];        // [row][lane of every token]
     __shared__ uint32_t s_group[GROUPED ? kScoredThreads * R : 1];
@@ -449,33 +484,59 @@ __global__ __launch_bounds__(kScoredThreads) void k_route_chunks(ScoredArgs a, C
     }
 
     uint32_t sel_key = 0u, sel_pos = 0u;
-    for (int r = 0; r < k; r++) {
-        uint32_t best = 0u;
+    if constexpr (SORTED) {
+        static_assert(R == 4, "sixteen candidates a lane");
+        double list[kList], more[kList];
 #pragma unroll
-        for (int i = 0; i < R; i++)
-#pragma unroll
-            for (int x = 0; x < 4; x++) best = best > c[i][x] ? best : c[i][x];
-        const uint32_t top = group_reduce<S>(best, UMax());
-        uint32_t pos = 0xFFFFFFFFu;                      // this lane's lowest holder
-#pragma unroll
-        for (int i = R - 1; i >= 0; i--)
-#pragma unroll
-            for (int x = 3; x >= 0; x--) pos = c[i][x] == top ? 4u * (g + S * i) + x : pos;
-        if constexpr (S == kWave) {
-            const uint64_t mask = __ballot(best == top);
-            if (__popcll(mask) == 1)
-                pos = (uint32_t)__builtin_amdgcn_readlane((int)pos, (int)__builtin_ctzll(mask));
-            else
-                pos = group_reduce<S>(pos, UMin());
-        } else {
-            pos = group_reduce<S>(pos, UMin());
+        for (int q = 0; q < kList; q++) {
+            const int i = q / 4, x = q % 4;
+            const int at = 4 * (g + S * i) + x, below = 4 * (g + S * (i + 2)) + x;
+            list[q] = c[i][x] ? key_pack(c[i][x], at) : kCandNone;
+            more[q] = c[i + 2][x] ? key_pack(c[i + 2][x], below) : kCandNone;
         }
+        sort_desc<kList>(list);
+        sort_desc<kList>(more);
+        merge_top<kList>(list, more);
+        join_lists<1>(list);
+        join_lists<2>(list);
+        join_lists<4>(list);
+        if constexpr (S > 8) join_lists<8>(list);
+        if constexpr (S > 16) join_lists<16>(list);
+        if constexpr (S > 32) join_lists<32>(list);
 #pragma unroll
-        for (int i = 0; i < R; i++)
+        for (int r = 0; r < kList; r++) {
+            sel_key = g == r ? cand_key(list[r]) : sel_key;
+            sel_pos = g == r ? (uint32_t)cand_expert(list[r]) : sel_pos;
+        }
+    } else {
+        for (int r = 0; r < k; r++) {
+            uint32_t best = 0u;
 #pragma unroll
-            for (int x = 0; x < 4; x++) c[i][x] = pos == 4u * (g + S * i) + x ? 0u : c[i][x];
-        sel_key = g == r ? top : sel_key;
-        sel_pos = g == r ? pos : sel_pos;
+            for (int i = 0; i < R; i++)
+#pragma unroll
+                for (int x = 0; x < 4; x++) best = best > c[i][x] ? best : c[i][x];
+            const uint32_t top = group_reduce<S>(best, UMax());
+            uint32_t pos = 0xFFFFFFFFu;                      // this lane's lowest holder
+#pragma unroll
+            for (int i = R - 1; i >= 0; i--)
+#pragma unroll
+                for (int x = 3; x >= 0; x--) pos = c[i][x] == top ? 4u * (g + S * i) + x : pos;
+            if constexpr (S == kWave) {
+                const uint64_t mask = __ballot(best == top);
+                if (__popcll(mask) == 1)
+                    pos = (uint32_t)__builtin_amdgcn_readlane((int)pos, (int)__builtin_ctzll(mask));
+                else
+                    pos = group_reduce<S>(pos, UMin());
+            } else {
+                pos = group_reduce<S>(pos, UMin());
+            }
+#pragma unroll
+            for (int i = 0; i < R; i++)
+#pragma unroll
+                for (int x = 0; x < 4; x++) c[i][x] = pos == 4u * (g + S * i) + x ? 0u : c[i][x];
+            sel_key = g == r ? top : sel_key;
+            sel_pos = g == r ? pos : sel_pos;
+        }
     }
 
     // weights: lane r has slot r
@@ -503,7 +564,7 @@ __global__ __launch_bounds__(kScoredThreads) void k_route_chunks(ScoredArgs a, C
 namespace {
 
 ChunkPlan chunk_plan(const ScoredArgs& a) {
-    ChunkPlan p{0, 1, 0, 0};
+    ChunkPlan p{0, 1, 0, 0, 0};
     const bool grouped = a.topk_group < a.n_group;
     const int per = grouped ? a.E / a.n_group : a.E;
     while (4 << p.cg_lg < per) p.cg_lg++;
@@ -511,13 +572,24 @@ ChunkPlan chunk_plan(const ScoredArgs& a) {
     // a block's rows have to fit a buffer descriptor
     if (slots > 4 * kWave || a.k > kWave || a.ld > (1 << 20)) return p;
     // One chunk per lane is quickest for one token; where many tokens share the
-    // chip, half the lanes with twice the chunks save instructions: 16384 tokens
-    // of 256 experts, 19.0 -> 16.9 us (sigmoid, 8 groups), 17.3 -> 14.4 us
-    // (softmax, no groups); a quarter of the lanes: 16.5 and 13.4 us there, but
-    // 6.4 -> 7.8 us with 4096 tokens of 160 experts.
+    // chip, fewer lanes with more chunks save instructions. Half the lanes: 16384
+    // tokens of 256 experts 19.0 -> 16.8 us (sigmoid, 8 groups), 17.3 -> 14.4 us
+    // (softmax, no groups). Four chunks a lane through the sorting networks: 14.5
+    // and 11.2 us; 2048 tokens of 384 experts 6.9 -> 5.2 us; but 6.4 -> 7.2 us for
+    // 4096 tokens of 160 experts in groups (too few waves to hide the chains),
+    // and 4.9 -> 6.7 us for 16384 tokens of 64 experts (mostly empty places).
     int lanes = 8;
     while (lanes < kWave && (lanes < slots || lanes < a.k)) lanes <<= 1;
     if (a.T >= 2048 && lanes > 8 && lanes / 2 >= a.k && slots <= lanes * 2) lanes >>= 1;
+    if (slots > 16 && a.k <= kList) {
+        int four = 8;
+        while (four * 4 < slots) four <<= 1;
+        p.sorted = a.T * four >= (grouped ? 1 << 17 : 1 << 16);
+        if (p.sorted) {
+            lanes = four;
+            p.rows = 4;
+        }
+    }
     while (p.rows * lanes < slots) p.rows <<= 1;
     p.lanes = lanes;
     const uintptr_t base = reinterpret_cast<uintptr_t>(a.logits);
@@ -525,14 +597,14 @@ ChunkPlan chunk_plan(const ScoredArgs& a) {
     return p;
 }
 
-template <int S, int R>
+template <int S, int R, bool SORTED = false>
 void launch_chunks(const ScoredArgs& a, const ChunkPlan& p, int64_t blocks, hipStream_t stream) {
     const dim3 grid((unsigned)blocks), block(kScoredThreads);
     const bool grouped = a.topk_group < a.n_group;
-    if (a.sigmoid && grouped) k_route_chunks<S, R, true, true><<<grid, block, 0, stream>>>(a, p);
-    else if (a.sigmoid) k_route_chunks<S, R, true, false><<<grid, block, 0, stream>>>(a, p);
-    else if (grouped) k_route_chunks<S, R, false, true><<<grid, block, 0, stream>>>(a, p);
-    else k_route_chunks<S, R, false, false><<<grid, block, 0, stream>>>(a, p);
+    if (a.sigmoid && grouped) k_route_chunks<S, R, SORTED, true, true><<<grid, block, 0, stream>>>(a, p);
+    else if (a.sigmoid) k_route_chunks<S, R, SORTED, true, false><<<grid, block, 0, stream>>>(a, p);
+    else if (grouped) k_route_chunks<S, R, SORTED, false, true><<<grid, block, 0, stream>>>(a, p);
+    else k_route_chunks<S, R, SORTED, false, false><<<grid, block, 0, stream>>>(a, p);
 }
 
 }  // namespace
@@ -545,6 +617,15 @@ hipError_t launch_route_scored(const ScoredArgs& a, hipStream_t stream, LaunchIn
         const int64_t blocks = (a.T + per_block - 1) / per_block;
         if (info) *info = LaunchInfo{blocks, kScoredThreads, 0, p.lanes, "route_chunks"};
         if (!run || blocks == 0) return hipSuccess;
+        if (p.sorted) {
+            switch (p.lanes) {
+                case 8: launch_chunks<8, 4, true>(a, p, blocks, stream); break;
+                case 16: launch_chunks<16, 4, true>(a, p, blocks, stream); break;
+                case 32: launch_chunks<32, 4, true>(a, p, blocks, stream); break;
+                default: launch_chunks<64, 4, true>(a, p, blocks, stream);
+            }
+            return hipGetLastError();
+        }
         switch (p.lanes * 8 + p.rows) {
             case 8 * 8 + 1: launch_chunks<8, 1>(a, p, blocks, stream); break;
             case 16 * 8 + 1: launch_chunks<16, 1>(a, p, blocks, stream); break;

@@ -200,6 +200,9 @@ def test_shared_slots_and_given_outputs():
     (9, 1024, 8, 1024, 100, 1), (7, 1000, 5, 500, 50, 2), (6, 1023, 9, 3, 2, 2), (4, 1024, 70, 2, 1, 2),
     (2100, 512, 8, 2, 1, 2), (2100, 1024, 4, 2, 1, 2), (2050, 40, 20, 5, 4, 1), (2048, 250, 8, 1, 1, 2),
     (3, 1024, 64, 1, 1, 2), (5, 1021, 33, 1, 1, 2), (2100, 12, 9, 2, 1, 2), (2060, 257, 12, 1, 1, 1),
+    # the sorted kernel with 8, 16, 32 and 64 lanes per token, with groups and without
+    (16400, 100, 5, 5, 3, 2), (8200, 256, 8, 8, 4, 2), (8300, 240, 8, 10, 4, 1), (4100, 512, 7, 2, 1, 2),
+    (2100, 1024, 8, 16, 5, 2), (2200, 1000, 3, 1, 1, 1), (8200, 70, 8, 1, 1, 1), (2050, 510, 1, 1, 1, 1),
 ])
 def test_many_groups_wide_groups_and_both_kernels(T, E, k, G, KG, top):
     """Groups of one expert, groups wider than the lanes, odd widths, k past the
