@@ -16,6 +16,12 @@ constexpr int64_t kInt32Max = 2147483647;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Byte ranges [p, p + n) and [q, q + m) share a byte.
+bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
+    const auto a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b ? b - a < (uint64_t)n : a - b < (uint64_t)m;
+}
+
 bool log_enabled() {
     static const int on = [] {
         const char* v = getenv("MOE_ROUTE_LOG");
@@ -456,6 +462,12 @@ int moe_grouped_gemm_bf16(const void* a, const int32_t* expert_offsets, const vo
     if (!aligned(a, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(bias, 16) ||
         !aligned(residual, 16) || !aligned(expert_offsets, 4))
         return MOE_EALIGN;
+    // a workgroup writes y while others still read a, w and the residual rows
+    const int64_t y_bytes = max_rows * (gated ? N / 2 : N) * 2;
+    if (overlap(y, y_bytes, a, max_rows * K * 2) || overlap(y, y_bytes, w, (int64_t)E * N * K * 2) ||
+        (bias && overlap(y, y_bytes, bias, (int64_t)E * N * 2)) ||
+        (residual && residual != y && overlap(y, y_bytes, residual, y_bytes)))
+        return MOE_EINVAL;
     const hipError_t e = moe::launch_grouped_gemm_bf16(g, static_cast<hipStream_t>(stream), &info);
     if (log_enabled()) log_launch(info.name, info);
     return status_of(e);
@@ -475,6 +487,11 @@ int moe_gated_act_quant_fp8(const void* h, const int32_t* expert_offsets, int E,
     if (!aligned(h, 16) || !aligned(out, 16) || !aligned(out_scales, 4) ||
         !aligned(expert_offsets, 4))
         return MOE_EALIGN;
+    // workgroups write out while others still read h
+    const int64_t h_bytes = max_rows * I * 4, o_bytes = max_rows * I, s_bytes = max_rows * (I / 32);
+    if (overlap(h, h_bytes, out, o_bytes) || overlap(h, h_bytes, out_scales, s_bytes) ||
+        overlap(out, o_bytes, out_scales, s_bytes))
+        return MOE_EINVAL;
     const hipError_t e = moe::launch_gated_act_fp8(h, expert_offsets, E, max_rows, I, act, out,
                                                    out_scales, static_cast<hipStream_t>(stream),
                                                    &info);

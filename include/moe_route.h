@@ -124,7 +124,9 @@ int moe_route_topk_shared(const float* logits, int64_t T, int E, int k, int n_sh
  *   topk_w       device, fp32 [T, k + n_shared] out
  *   1 <= k <= topk_group * E / n_group; E % n_group == 0;
  *   1 <= topk_group <= n_group; group_top 1 or 2;
- *   E + n_shared <= MOE_MAX_EXPERTS; T >= 0 (T == 0 is a no-op).
+ *   E + n_shared <= MOE_MAX_EXPERTS; T >= 0 (T == 0 is a no-op);
+ *   T * (k + n_shared) < 2^31, ld_logits <= 2^31, T * ld_logits <= 2^40, and
+ *   the launch has to fit a packet (64 T < 2^32 at most).
  */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 typedef enum { MOE_LOGITS_F32 = 0, MOE_LOGITS_BF16 = 1 } moe_logits_dtype;
@@ -398,8 +400,9 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GEL
  *   E, N, K         1 <= E <= 1024; 8 <= K <= 2^20, K % 8 == 0;
  *                   8 <= N <= 2^20, N % 8 == 0 (N % 16 == 0 when gated)
  *   max_rows        rows of a, residual and y; 0 <= max_rows < 2^31
- * y overlaps neither a nor w. No workspace; nothing is kept between calls.
- * Errors: MOE_EINVAL (limits, launch size), MOE_ENULL, MOE_EALIGN, MOE_EHIP.
+ * No workspace; nothing is kept between calls. Errors: MOE_EINVAL (limits,
+ * launch size, y overlapping a, w, bias or part of residual), MOE_ENULL,
+ * MOE_EALIGN, MOE_EHIP.
  * max_rows == 0 returns MOE_OK without a launch.
  */
 int moe_grouped_gemm_bf16(const void* a, const int32_t* expert_offsets, const void* w,
@@ -423,8 +426,8 @@ int moe_grouped_gemm_bf16(const void* a, const int32_t* expert_offsets, const vo
  *   I % 128 == 0, 128 <= I <= 2^20; 0 <= max_rows < 2^31; 1 <= E <= 1024
  * out and out_scales are the a and a_scales of the next moe_grouped_gemm_fp8.
  * Rows at or past expert_offsets[E] are neither read nor written; pad rows
- * of a segment (zeros) give zero codes and scales. max_rows == 0 returns
- * MOE_OK without a launch.
+ * of a segment (zeros) give zero codes and scales. h, out and out_scales do
+ * not overlap (MOE_EINVAL). max_rows == 0 returns MOE_OK without a launch.
  */
 int moe_gated_act_quant_fp8(const void* h, const int32_t* expert_offsets, int E, int64_t max_rows,
                             int I, int act, void* out, float* out_scales, void* stream);

@@ -86,6 +86,22 @@ def test_gemm_bf16_pointers():
     assert gemm(R=0, a=None, off=None, w=None, y=None) == OK
 
 
+def test_gemm_bf16_overlaps():
+    """y on top of an operand is refused (every call here overlaps, so nothing
+    is launched); the residual may be y itself only."""
+    y = A + 2 ** 26                                  # 1000 x 512 bf16
+    end = y + 1000 * 512 * 2
+    for p in ("a", "w", "bias", "res"):
+        for at in (y + 16, end - 16):
+            assert gemm(**{p: at}) == EINVAL, p
+    for p in ("a", "w", "bias"):
+        assert gemm(**{p: y}) == EINVAL, p
+    assert gemm(a=y - 1000 * 256 * 2 + 16) == EINVAL
+    assert gemm(w=y - 8 * 512 * 256 * 2 + 16) == EINVAL
+    assert gemm(res=y - 1000 * 512 * 2 + 16) == EINVAL
+    assert gemm(gated=1, res=y + 1000 * 256 * 2 - 16) == EINVAL
+
+
 def gact(**kw):
     a = dict(h=A, off=B, E=8, R=1000, I=256, act=2, out=A + 2 ** 24, sc=B + 2 ** 20)
     a.update(kw)
@@ -103,4 +119,10 @@ def test_gated_act_refusals():
     assert gact(out=A + 2 ** 24 + 8) == EALIGN
     assert gact(sc=B + 2) == EALIGN
     assert gact(off=B + 1) == EALIGN
+    out = A + 2 ** 24                                # 1000 x 256 codes
+    assert gact(h=out) == EINVAL
+    assert gact(h=out - 1000 * 512 * 2 + 16) == EINVAL
+    assert gact(h=out + 1000 * 256 - 64) == EINVAL
+    assert gact(sc=out + 64) == EINVAL
+    assert gact(sc=A + 64) == EINVAL
     assert gact(R=0, h=None, off=None, out=None, sc=None) == OK
