@@ -3,7 +3,7 @@
 //   v[c] = act(h[c]) * h[I + c]                       (fp32)
 //   s    = max |v| over 128 channels / 448            (fp32)
 //   code = E4M3(v / s), nearest even, saturated; s == 0 gives zero codes
-// the same quantisation as the FP8 dispatch. Bound by memory: 4 I bytes read
+// (v past fp32's range counts as the largest finite value), the same quantisation as the FP8 dispatch. Bound by memory: 4 I bytes read
 // and I + I / 32 written a row. 147 thousand rows of 2048 channels (1.51 GB):
 // 243 us, 6.2 TB/s.
 //
@@ -28,6 +28,7 @@ namespace {
 constexpr int kGatedThreads = 256;
 constexpr int kUnits = kGatedThreads / 16;   // 128-channel blocks a workgroup takes at a time
 constexpr int kDepth = 2;                    // blocks of a lane in flight
+constexpr float kMaxFloat = 0x1.fffffep127f; // largest finite fp32
 
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
@@ -107,12 +108,20 @@ __global__ __launch_bounds__(kGatedThreads) void k_gated_act_fp8(
                 v[i] = gated_product<ACT>(g[i], v[i]);
                 amax = fmaxf(amax, fabsf(v[i]));
             }
-            if (!(pmax < INFINITY)) {                    // g u out of range, act(g) u maybe not
+            // g u out of range: then |u| > 1, and 2^-128 u keeps its bits. act(g) u may be in
+            // range; if not, the largest finite value stands for it (|act(g)| <= |g|, so
+            // only here): an infinite v or s would make NaN of the whole block below.
+            if (!(pmax < INFINITY)) {
                 amax = 0.0f;
-                unpack8(make_uint4(u4[d][0], u4[d][1], u4[d][2], u4[d][3]), v);
+                float u[8];
+                unpack8(make_uint4(u4[d][0], u4[d][1], u4[d][2], u4[d][3]), u);
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    v[i] *= activate<ACT>(g[i]);
+                    if (!(fabsf(g[i] * u[i]) < INFINITY)) {
+                        v[i] = gated_product<ACT>(g[i], u[i] * 0x1p-64f * 0x1p-64f);
+                        v[i] = v[i] * 0x1p64f * 0x1p64f;
+                        v[i] = v[i] > kMaxFloat ? kMaxFloat : v[i] < -kMaxFloat ? -kMaxFloat : v[i];
+                    }
                     amax = fmaxf(amax, fabsf(v[i]));
                 }
             }

@@ -413,7 +413,8 @@ int moe_grouped_gemm_bf16(const void* a, const int32_t* expert_offsets, const vo
  * Gated activation between the two FP8 grouped GEMMs. For every row r below
  * expert_offsets[E] (clamped to max_rows) and block b of 128 channels:
  *
- *   v[c]  = act(h[r, c]) * h[r, I + c]                    (fp32)
+ *   v[c]  = act(h[r, c]) * h[r, I + c]                    (fp32; past its range the
+ *           largest finite value of the sign, so that s and the codes stay finite)
  *   s     = max |v| over the block / 448                  (fp32)
  *   out   = E4M3 codes of v / s, nearest even, saturated to +-448; a block
  *           whose s is 0 gets zero codes (moe_dispatch's quantisation)
