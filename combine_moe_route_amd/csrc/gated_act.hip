@@ -51,7 +51,9 @@ __device__ __forceinline__ float gated_product(float g, float u) {
         const float d = 1.0f + e;
         float r = __builtin_amdgcn_rcpf(d);
         r = fmaf(fmaf(-d, r, 1.0f), r, r);
-        return d < INFINITY ? p * r : 0.0f;              // g below -88
+        // d is inf for g below -88.7; it stays NaN for a NaN gate. A reciprocal below
+        // 2^-126 (g below -87.3) may count as 0.
+        return d == INFINITY ? 0.0f : p * r;
     }
     if constexpr (ACT == kActGelu) {
         const float d = fmaf(0.21213203435596426f, fabsf(g), 1.0f);

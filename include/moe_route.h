@@ -369,7 +369,8 @@ int moe_grouped_gemm_fp8(const void* a, const float* a_scales, const int32_t* ex
                          void* stream);
 
 /* Activations of the experts, in fp32: none, max(z, 0), z * sigmoid(z),
- * z/2 * erfc(-z/sqrt 2). */
+ * z/2 * erfc(-z/sqrt 2). Factors of z below 2^-126 may count as 0 (silu of z
+ * below -87.3, gelu of z below -13.2). */
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 } moe_act;
 
 /*

@@ -1,5 +1,5 @@
 """moe_gated_act_quant_fp8 where fp32 ends: products past its range, gates whose
-exponential leaves it, and that calls repeat.
+exponential leaves it, a NaN among finite values, and that calls repeat.
 
 Tolerances as in test_gpu_gated_act.py (scale, half an E4M3 step, division),
 with the activation's own error per test.
@@ -95,6 +95,25 @@ def test_silu_gates_far_below_zero():
         h[r, I:] = 2.0 ** 119 * (1 + torch.arange(I, device=DEV) / I)
     compare(h, "silu", lambda g, u, v: 2.0 ** -20 * v.abs() + torch.where(
         g < -87.3, 2.0 ** -126 * (g * u).abs(), 0.0))
+
+
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+def test_nan_stays_nan(act):
+    """A NaN in either half has the code of NaN; the block's other values are
+    those of the block with a zero in its place."""
+    log(f"gated_act NaN {act}")
+    I = 256
+    h = normal(4, I, 6)
+    zero = h.clone()
+    for r, c in ((0, 5), (1, I + 5), (2, 200), (3, I + 255)):
+        h[r, c] = float("nan")
+        zero[r, c] = 0
+    out, sc = run(h, [0, 4], act)
+    o0, s0 = run(zero, [0, 4], act)
+    hit = torch.isnan(h[:, :I]) | torch.isnan(h[:, I:])
+    assert hit.sum() == 4
+    assert (out[hit] & 0x7F == 0x7F).all()
+    assert torch.equal(out[~hit], o0[~hit]) and torch.equal(sc, s0)
 
 
 @pytest.mark.parametrize("act", ACTS)
