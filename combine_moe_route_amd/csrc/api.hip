@@ -462,9 +462,10 @@ int moe_grouped_gemm_bf16(const void* a, const int32_t* expert_offsets, const vo
     if (!aligned(a, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(bias, 16) ||
         !aligned(residual, 16) || !aligned(expert_offsets, 4))
         return MOE_EALIGN;
-    // a workgroup writes y while others still read a, w and the residual rows
+    // a workgroup writes y while others still read the offsets, a, w and the residual rows
     const int64_t y_bytes = max_rows * (gated ? N / 2 : N) * 2;
     if (overlap(y, y_bytes, a, max_rows * K * 2) || overlap(y, y_bytes, w, (int64_t)E * N * K * 2) ||
+        overlap(y, y_bytes, expert_offsets, ((int64_t)E + 1) * 4) ||
         (bias && overlap(y, y_bytes, bias, (int64_t)E * N * 2)) ||
         (residual && residual != y && overlap(y, y_bytes, residual, y_bytes)))
         return MOE_EINVAL;
@@ -487,10 +488,12 @@ int moe_gated_act_quant_fp8(const void* h, const int32_t* expert_offsets, int E,
     if (!aligned(h, 16) || !aligned(out, 16) || !aligned(out_scales, 4) ||
         !aligned(expert_offsets, 4))
         return MOE_EALIGN;
-    // workgroups write out while others still read h
+    // workgroups write out while others still read h and the number of rows
     const int64_t h_bytes = max_rows * I * 4, o_bytes = max_rows * I, s_bytes = max_rows * (I / 32);
+    const int64_t e_bytes = ((int64_t)E + 1) * 4;
     if (overlap(h, h_bytes, out, o_bytes) || overlap(h, h_bytes, out_scales, s_bytes) ||
-        overlap(out, o_bytes, out_scales, s_bytes))
+        overlap(out, o_bytes, out_scales, s_bytes) || overlap(expert_offsets, e_bytes, out, o_bytes) ||
+        overlap(expert_offsets, e_bytes, out_scales, s_bytes))
         return MOE_EINVAL;
     const hipError_t e = moe::launch_gated_act_fp8(h, expert_offsets, E, max_rows, I, act, out,
                                                    out_scales, static_cast<hipStream_t>(stream),

@@ -370,7 +370,7 @@ int moe_grouped_gemm_fp8(const void* a, const float* a_scales, const int32_t* ex
 
 /* Activations of the experts, in fp32: none, max(z, 0), z * sigmoid(z),
  * z/2 * erfc(-z/sqrt 2). Factors of z below 2^-126 may count as 0 (silu of z
- * below -87.3, gelu of z below -13.2). */
+ * below -87.3, gelu of z below -12.9). */
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 } moe_act;
 
 /*
@@ -402,8 +402,8 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GEL
  *                   8 <= N <= 2^20, N % 8 == 0 (N % 16 == 0 when gated)
  *   max_rows        rows of a, residual and y; 0 <= max_rows < 2^31
  * No workspace; nothing is kept between calls. Errors: MOE_EINVAL (limits,
- * launch size, y overlapping a, w, bias or part of residual), MOE_ENULL,
- * MOE_EALIGN, MOE_EHIP.
+ * launch size, y overlapping a, expert_offsets, w, bias or part of residual),
+ * MOE_ENULL, MOE_EALIGN, MOE_EHIP.
  * max_rows == 0 returns MOE_OK without a launch.
  */
 int moe_grouped_gemm_bf16(const void* a, const int32_t* expert_offsets, const void* w,
@@ -428,8 +428,8 @@ int moe_grouped_gemm_bf16(const void* a, const int32_t* expert_offsets, const vo
  *   I % 128 == 0, 128 <= I <= 2^20; 0 <= max_rows < 2^31; 1 <= E <= 1024
  * out and out_scales are the a and a_scales of the next moe_grouped_gemm_fp8.
  * Rows at or past expert_offsets[E] are neither read nor written; pad rows
- * of a segment (zeros) give zero codes and scales. h, out and out_scales do
- * not overlap (MOE_EINVAL). max_rows == 0 returns MOE_OK without a launch.
+ * of a segment (zeros) give zero codes and scales. out and out_scales overlap
+ * neither each other nor h nor expert_offsets (MOE_EINVAL). max_rows == 0 returns MOE_OK without a launch.
  */
 int moe_gated_act_quant_fp8(const void* h, const int32_t* expert_offsets, int E, int64_t max_rows,
                             int I, int act, void* out, float* out_scales, void* stream);
