@@ -22,6 +22,18 @@ bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
     return a < b ? b - a < (uint64_t)n : a - b < (uint64_t)m;
 }
 
+// Byte range [p, p + n) shares a byte with one of `rows` rows of `width` bytes,
+// the first at q, `step` bytes apart (step >= width). The last row that starts
+// before p + n is the only one that has to be looked at.
+bool overlap_rows(const void* p, int64_t n, const void* q, int64_t rows, int64_t step,
+                  int64_t width) {
+    const auto a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    if (rows == 0 || a + (uint64_t)n <= b) return false;
+    const uint64_t last = (a + (uint64_t)n - 1 - b) / (uint64_t)step;
+    const uint64_t row = last < (uint64_t)rows ? last : (uint64_t)rows - 1;
+    return a < b + row * (uint64_t)step + (uint64_t)width;
+}
+
 bool log_enabled() {
     static const int on = [] {
         const char* v = getenv("MOE_ROUTE_LOG");
@@ -429,6 +441,13 @@ int moe_route_scored(const void* logits, int logits_dtype, int64_t ld_logits, in
     if (!aligned(logits, a.bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(topk_idx, 4) ||
         !aligned(topk_w, 4))
         return MOE_EALIGN;
+    // tokens are written while others still read their logits and the bias
+    const int64_t size = a.bf16 ? 2 : 4, o_bytes = T * (k + n_shared) * 4;
+    for (const void* out : {static_cast<const void*>(topk_idx), static_cast<const void*>(topk_w)})
+        if (overlap_rows(out, o_bytes, logits, T, ld_logits * size, E * size) ||
+            (bias && overlap(out, o_bytes, bias, (int64_t)E * 4)))
+            return MOE_EINVAL;
+    if (overlap(topk_idx, o_bytes, topk_w, o_bytes)) return MOE_EINVAL;
     const hipError_t e = moe::launch_route_scored(a, static_cast<hipStream_t>(stream), &info);
     if (log_enabled()) log_launch(info.name, info);
     return status_of(e);

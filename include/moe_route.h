@@ -126,7 +126,9 @@ int moe_route_topk_shared(const float* logits, int64_t T, int E, int k, int n_sh
  *   1 <= topk_group <= n_group; group_top 1 or 2;
  *   E + n_shared <= MOE_MAX_EXPERTS; T >= 0 (T == 0 is a no-op);
  *   T * (k + n_shared) < 2^31, ld_logits <= 2^31, T * ld_logits <= 2^40, and
- *   the launch has to fit a packet (64 T < 2^32 at most).
+ *   the launch has to fit a packet (64 T < 2^32 at most). topk_idx and topk_w
+ *   overlap neither each other nor bias nor a row of logits (the gaps between
+ *   rows are free); MOE_EINVAL otherwise.
  */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 typedef enum { MOE_LOGITS_F32 = 0, MOE_LOGITS_BF16 = 1 } moe_logits_dtype;
