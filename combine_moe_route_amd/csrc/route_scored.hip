@@ -14,9 +14,12 @@
 // off would choose another expert. After that rounding the choice is exact
 // fp32 comparisons and additions, ties to the lower index.
 //
-// Two kernels, both with k rounds of a maximum over the lanes of a token:
-// k_route_chunks for rows of up to 256 chunks of four experts and k up to its
-// lanes per token, k_route_rounds for every other shape.
+// Two kernels. k_route_chunks cuts a row into chunks of four experts and takes k
+// up to 64, rows at most 2^20 elements apart and at most 256 chunks, where each
+// group's count is filled up to a power of two; the choice is k rounds of a
+// maximum over the lanes of a token, or sorting networks. k_route_rounds takes
+// the rest: k above 64, rows further apart, and wide groups whose filled counts
+// pass 256 (five groups of 129 to 204 experts: 5 x 64).
 #include "launch.h"
 #include "moe_device.h"
 #include "topk_sort.h"
@@ -40,7 +43,8 @@ struct FMax {
 };
 
 // exp(y) in fp64 for |y| <= 150: y = n ln 2 + r with |r| <= ln 2 / 2 (Cody and
-// Waite's reduction, ln 2 in two parts), the Taylor series of exp(r) to r^12 / 12! (the next term is below 2^-52), times 2^n.
+// Waite's reduction, ln 2 in two parts), the Taylor series of exp(r) to
+// r^12 / 12! (the next term is below 2^-52), times 2^n.
 // A score rounded to fp32 from it differs from the right rounding only where
 // the exact value lies within about 2^-51 of a midpoint between two floats,
 // once in 2^25 values.
@@ -100,7 +104,8 @@ __device__ __forceinline__ uint32_t choice_key(float v) {
 
 }  // namespace
 
-// One wave per token, experts lane, lane + 64, ... (any E, k, group count).
+// One wave per token, experts lane, lane + 64, ... (any E, k, group count). With
+// groups, lane g scans group g serially.
 // LDS per wave: scores [E], keys [E] (reused by the group stage), chosen
 // experts [k], group keys [n_group].
 template <int NV>
