@@ -634,14 +634,15 @@ hipError_t launch_shape(const GemmBf16Args& g, hipStream_t stream, LaunchInfo* i
     const int64_t max_tiles = (g.max_rows + SH::kBM - 1) / SH::kBM + g.E;
     const int64_t items = max_tiles * ((n_out + out_cols - 1) / out_cols);
     const int64_t grid = (items + kXcds - 1) / kXcds * kXcds;
+    constexpr bool kStreamed = std::is_same_v<SH, Skinny<true>>;
     if (info)
-        *info = LaunchInfo{grid, SH::kThreads, (size_t)SH::kLds, SH::kBM, "grouped_gemm_bf16"};
+        *info = LaunchInfo{grid, SH::kThreads, (size_t)SH::kLds, SH::kBM,
+                           kStreamed ? "streamed_grouped_gemm_bf16" : "grouped_gemm_bf16"};
     if (!run) return hipSuccess;
     const dim3 blocks((unsigned)grid), threads(SH::kThreads);
     if constexpr (SH::kBN == 64) {
-        constexpr bool S = std::is_same_v<SH, Skinny<true>>;
-        if (g.gated) k_grouped_gemm_bf16_skinny<S, true><<<blocks, threads, 0, stream>>>(g);
-        else k_grouped_gemm_bf16_skinny<S, false><<<blocks, threads, 0, stream>>>(g);
+        if (g.gated) k_grouped_gemm_bf16_skinny<kStreamed, true><<<blocks, threads, 0, stream>>>(g);
+        else k_grouped_gemm_bf16_skinny<kStreamed, false><<<blocks, threads, 0, stream>>>(g);
     } else {
         if (g.gated) k_grouped_gemm_bf16<SH, true><<<blocks, threads, 0, stream>>>(g);
         else k_grouped_gemm_bf16<SH, false><<<blocks, threads, 0, stream>>>(g);

@@ -4,6 +4,11 @@ The shape goes by the capacity (rows of a over the experts), N and K, so small
 ragged segments in a large buffer reach each of them; the tolerance is that of
 test_gpu_gemm_bf16.py.
 """
+import os
+import re
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -13,6 +18,10 @@ from test_gpu_gemm_bf16 import case, run
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+# (rows of a tile, threads) of a shape in the launch log
+LOGGED = {"large": (256, 256), "medium": (128, 512), "small": (128, 256), "skinny": (32, 256)}
 
 # shape: (experts, capacity, N, inner sizes: one k-block to several turns of the
 # ring with every remainder, and odd tails). The last column tile holds 16 columns,
@@ -38,6 +47,9 @@ def shape_case(shape, K, gated, bias=False, residual=False, seed=None):
                 gated=gated, first=0 if shape == "skinny" else 5)
 
 
+ALL = [(s, K, g) for s in SHAPES for K in SHAPES[s][3] for g in (False, True)]
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("shape", list(SHAPES))
@@ -61,3 +73,23 @@ def test_infinite_sums(shape, gated, act):
     # the sum of positive terms is off by K 2^-23 of itself, squared when gated
     tol = 2.0 ** -8 + 3 * c["a"].shape[1] * 2.0 ** -23
     assert ((y[r + 2].double() - want).abs() <= tol * want).all()
+
+
+def test_shapes_reached():
+    """From the launch log, read in a child process: each case above runs on the
+    shape it is listed under, and rows of whole 128-byte lines are streamed by
+    the skinny tiles of small capacities, others not."""
+    cases = [(s, K, g) for s, K, g in ALL]
+    code = ("import sys; sys.path.insert(0, 'tests')\n"
+            "from test_gpu_gemm_bf16_shapes import shape_case\n"
+            "from test_gpu_gemm_bf16 import run\n"
+            f"for s, K, g in {cases!r}:\n"
+            "    run(shape_case(s, K, g), 'none')\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                       timeout=110, env=dict(os.environ, MOE_ROUTE_LOG="1"))
+    assert r.returncode == 0, r.stderr[-2000:]
+    got = re.findall(r"(\w*)grouped_gemm_bf16 grid=\d+ block=(\d+) lds=\d+ param=(\d+)", r.stderr)
+    assert len(got) == len(cases)
+    for (shape, K, _), (prefix, block, rows) in zip(cases, got):
+        assert (int(rows), int(block)) == LOGGED[shape], (shape, K)
+        assert (prefix == "streamed_") == (shape == "skinny" and K % 64 == 0), (shape, K, prefix)
