@@ -110,20 +110,16 @@ __global__ __launch_bounds__(kGatedThreads) void k_gated_act_fp8(
                 v[i] = gated_product<ACT>(g[i], v[i]);
                 amax = fmaxf(amax, fabsf(v[i]));
             }
-            // g u out of range: then |u| > 1, and 2^-128 u keeps its bits. act(g) u may be in
-            // range; if not, the largest finite value stands for it (|act(g)| <= |g|, so
-            // only here): an infinite v or s would make NaN of the whole block below.
+            // g u out of range: act(g) u maybe not. If it is, the largest finite value
+            // stands for it (|act(g)| <= |g|, so only here): an infinite v or s would
+            // make NaN of the whole block below.
             if (!(pmax < INFINITY)) {
                 amax = 0.0f;
-                float u[8];
-                unpack8(make_uint4(u4[d][0], u4[d][1], u4[d][2], u4[d][3]), u);
+                unpack8(make_uint4(u4[d][0], u4[d][1], u4[d][2], u4[d][3]), v);
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    if (!(fabsf(g[i] * u[i]) < INFINITY)) {
-                        v[i] = gated_product<ACT>(g[i], u[i] * 0x1p-64f * 0x1p-64f);
-                        v[i] = v[i] * 0x1p64f * 0x1p64f;
-                        v[i] = v[i] > kMaxFloat ? kMaxFloat : v[i] < -kMaxFloat ? -kMaxFloat : v[i];
-                    }
+                    v[i] *= activate<ACT>(g[i]);
+                    v[i] = v[i] > kMaxFloat ? kMaxFloat : v[i] < -kMaxFloat ? -kMaxFloat : v[i];
                     amax = fmaxf(amax, fabsf(v[i]));
                 }
             }
