@@ -3,9 +3,12 @@
 //   v[c] = act(h[c]) * h[I + c]                       (fp32)
 //   s    = max |v| over 128 channels / 448            (fp32)
 //   code = E4M3(v / s), nearest even, saturated; s == 0 gives zero codes
-// (v past fp32's range counts as the largest finite value), the same quantisation as the FP8 dispatch. Bound by memory: 4 I bytes read
-// and I + I / 32 written a row. 147 thousand rows of 2048 channels (1.51 GB):
-// 243 us, 6.2 TB/s.
+// (v past fp32's range counts as the largest finite value), the same
+// quantisation as the FP8 dispatch. 4 I bytes read and I + I / 32 written a row:
+// 147 thousand rows of 2048 channels (1.51 GB) 243 us, 6.2 TB/s. There memory and
+// instructions are both near their limits (counters: 27.5 vector instructions a
+// value with SiLU, which at four cycles each fill 97 % of the cycles); GELU with
+// 6185 rows of 1408 is bound by instructions (96 %).
 //
 // 16 lanes own one block of 128 channels (8 channels, two 16-byte loads and one
 // 8-byte store each); the block's maximum is a DPP butterfly. A lane has up to
@@ -32,15 +35,15 @@ constexpr float kMaxFloat = 0x1.fffffep127f; // largest finite fp32
 
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
-// act(g) * u for bf16 g and u, close to one fp32 rounding (an error of v moves
+// act(g) * u for bf16 g and u, as close as fp32 steps come (an error of v moves
 // the codes that lie at a rounding border). g u is exact in fp32, so the gate's
 // factor is multiplied in last. The arguments of the exponentials are exact too:
 // log2 e is split so that its upper part times a bf16 value fits fp32, or the
 // product's rounding error is kept, and the rest corrects the result to first
-// order; the reciprocals get a Newton step. Of 33 million codes 25 to 43 then
-// differ from those of 64-bit arithmetic with silu and 43 to 52 with gelu (the
-// rounding of s alone moves most of them); fp32 with correctly rounded exp, erf
-// and divisions 29 to 47 and 63 to 89.
+// order; the reciprocals get a Newton step. Of 33 million codes 31 to 49 then
+// differ from those of 64-bit arithmetic with silu and 39 to 60 with gelu (the
+// rounding of s alone moves most of them); fp32 with the library's exp, erf and
+// divisions 32 to 51 and 64 to 93.
 template <int ACT>
 __device__ __forceinline__ float gated_product(float g, float u) {
     const float p = g * u;

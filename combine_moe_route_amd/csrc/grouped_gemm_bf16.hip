@@ -538,7 +538,8 @@ __global__ __launch_bounds__(Skinny<STREAM>::kThreads, 2) void k_grouped_gemm_bf
     // this wave's k-blocks: wave + 4 ((i + turn) mod n). Every tile starts at
     // another place, so that workgroups that run in step do not all read the
     // same columns of rows a power of two apart, which are the same memory
-    // channels (the 47 us above are 67 us without this; K 7168 is not affected).
+    // channels (one token through 2 of 8 experts, K 4096, N 16384: 46 us, without
+    // this 67; K 7168 is not affected).
     const int n = (KB - wave + kWaves - 1) / kWaves;
     const int turn = n > 0 ? nt % n : 0;
     auto issue = [&](auto stage, int i) {
@@ -655,11 +656,17 @@ hipError_t launch_shape(const GemmBf16Args& g, hipStream_t stream, LaunchInfo* i
 // The shape of a call, from what the host knows: the capacity, from which the
 // rows of an expert that has any, r (with padded segments more than there are).
 //
-// r <= 32: every weight is read about once and nothing else counts: Skinny.
-// With rows of whole 128-byte lines (K % 64 == 0) the weights are streamed: 128
-// tokens over 256 experts, K 7168, N 4096 (gated): 2000 us (7.4 TB/s), 2261 us
-// without the hint, 2300 us with Medium tiles. Lines shared by two k-blocks
-// would be fetched twice (18 tokens, K 2200: 49 us streamed, 38 us not).
+// r <= 32: Skinny, whose tile holds a segment of average length, so that segments
+// of like length read their weights once. A longer one reads them again: 256
+// experts, K 7168, N 4096 (gated), ragged segments of mean r, us:
+//   r           4     8    12    16    24    32
+//   Skinny   2000  2136  2198  2308  2910  3575
+//   Medium   2291  2363  2374  2385  2417  2495
+// For such segments the border would be better at about 18; the host does not know
+// how ragged they are. With rows of whole 128-byte lines (K % 64 == 0) the weights
+// are streamed: r = 4 above is 2000 us (7.4 TB/s), 2261 us without the hint. Lines
+// shared by two k-blocks would be fetched twice (18 tokens, K 2200: 49 us streamed,
+// 38 us not).
 //
 // Otherwise the shape of least estimated time: rounds of the chip times the
 // time of a round, start + k-blocks times a rate (us), fitted to:
@@ -673,7 +680,10 @@ hipError_t launch_shape(const GemmBf16Args& g, hipStream_t stream, LaunchInfo* i
 //    1 x 128, 4096, 4096                 70      41     35      20
 //    5 x 217, 416, 4584                  84      66     46      23
 // A segment ends inside a tile, half a tile on average; a lone segment's tiles
-// are known. The last round counts a quarter more than its share.
+// are known. The last round counts a quarter more than its share. Padded segments
+// of few tokens count as their capacity (one token through 8 of 256 experts, 128-row
+// segments, K 7168, N 4096: Medium 126 us, Small 127, Skinny, whose grid over the
+// capacity has 163 thousand workgroups, 422).
 hipError_t launch_grouped_gemm_bf16(const GemmBf16Args& g, hipStream_t stream, LaunchInfo* info,
                                     bool run) {
     const int64_t hit = g.E < g.max_rows ? g.E : g.max_rows;

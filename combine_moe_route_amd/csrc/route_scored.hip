@@ -305,10 +305,13 @@ __device__ __forceinline__ float across(float v) {
 // and the maximum is unique, else a minimum over the lanes. Lane r keeps the
 // winner of round r.
 //
-// Bound by instructions, about half of them the fp64 scores: 16384 tokens, 256
-// experts in 8 groups, k 8, sigmoid with bias 14.5 us (1.2 TB/s; the first
-// kernel, one token per wave with the device library's exp and a serial group
-// scan, took 29.9 us); one token 4.1 us (7.3 us). Tried: sorting with 8 lanes
+// Large batches are bound by instructions: 16384 tokens, 256 experts in 8 groups,
+// k 8, sigmoid with bias take 103 vector instructions a logit and lane, about 26 of
+// them the fp64 score; at four cycles each they fill 79 % of the cycles (counters).
+// 5003 tokens of 160 experts in groups are bound by latency: 59 %, 2.4 waves per
+// SIMD, which wait half of their time. The first case takes 14.5 us (1.2 TB/s; the
+// first kernel, one token per wave with the device library's exp and a serial group
+// scan, took 29.9 us), one token 4.1 us (7.3 us). Tried: sorting with 8 lanes
 // per token and keys waiting in LDS, 19.2 us and 13.0 us; every lane then works
 // through 32 experts in series.
 template <int S, int R, bool SORTED, bool SIGMOID, bool GROUPED>
