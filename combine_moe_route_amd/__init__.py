@@ -13,18 +13,23 @@ _API = (
     "DispatchBuffers",
     "MoeRouteError",
     "alloc_dispatch",
+    "alloc_dispatch_quantized",
     "moe_combine",
     "moe_combine_recv",
     "moe_combine_send",
     "moe_dispatch",
     "moe_dispatch_max_rows",
     "moe_dispatch_no_alloc",
+    "moe_dispatch_quantized",
     "moe_dispatch_workspace_bytes",
     "moe_gated_act_quant_fp8",
+    "moe_gated_act_quant_int8",
     "moe_grouped_gemm_bf16",
     "moe_grouped_gemm_fp8",
+    "moe_grouped_gemm_int8",
     "moe_grouped_gemm_workspace_bytes",
     "moe_harness_expert_scale",
+    "moe_rmsnorm_quant",
     "moe_route_dispatch",
     "moe_route_replicas",
     "moe_route_scored",

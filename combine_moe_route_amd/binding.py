@@ -23,6 +23,7 @@ MOE_OUT_BF16, MOE_OUT_FP8_E4M3 = 0, 1
 MOE_MAX_EXPERTS = 1024
 MOE_SCORES = {"softmax": 0, "sigmoid": 1}
 MOE_LOGITS = {torch.float32: 0, torch.bfloat16: 1}
+MOE_QUANTS = {"int8": 0, "fp8": 1}
 MOE_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 MOE_NO_ALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -36,6 +37,8 @@ EXPORTS = (
     "moe_dispatch_workspace_bytes",
     "moe_dispatch",
     "moe_dispatch_no_alloc",
+    "moe_dispatch_quantized",
+    "moe_rmsnorm_quant",
     "moe_route_dispatch",
     "moe_combine",
     "moe_combine_send",
@@ -43,7 +46,9 @@ EXPORTS = (
     "moe_grouped_gemm_workspace_bytes",
     "moe_grouped_gemm_fp8",
     "moe_grouped_gemm_bf16",
+    "moe_grouped_gemm_int8",
     "moe_gated_act_quant_fp8",
+    "moe_gated_act_quant_int8",
     "moe_harness_expert_scale",
     "moe_status_string",
 )
@@ -100,6 +105,15 @@ def _load() -> ctypes.CDLL:
     lib.moe_grouped_gemm_bf16.restype = i32
     lib.moe_gated_act_quant_fp8.argtypes = [P, P, i32, i64, i32, i32, P, P, P]
     lib.moe_gated_act_quant_fp8.restype = i32
+    lib.moe_dispatch_quantized.argtypes = [P, P, P, i64, i32, i32, i32, i32, i32, i32, P, P, P, P,
+                                           P, P, P, P, ctypes.c_size_t, P]
+    lib.moe_dispatch_quantized.restype = i32
+    lib.moe_rmsnorm_quant.argtypes = [P, i64, P, P, i64, i32, f32, i32, P, P, P, P, P]
+    lib.moe_rmsnorm_quant.restype = i32
+    lib.moe_grouped_gemm_int8.argtypes = [P, P, P, P, P, P, P, i32, i32, i32, i64, i32, i32, P, P]
+    lib.moe_grouped_gemm_int8.restype = i32
+    lib.moe_gated_act_quant_int8.argtypes = [P, P, i32, i64, i32, i32, P, P, P]
+    lib.moe_gated_act_quant_int8.restype = i32
     lib.moe_harness_expert_scale.argtypes = [P, P, P, P, P, i64, i32, i32, i32, i32, P, P]
     lib.moe_harness_expert_scale.restype = i32
     lib.moe_status_string.argtypes = [i32]
@@ -271,8 +285,8 @@ def moe_dispatch_workspace_bytes(T: int, E: int, k: int, groups: int = 1) -> int
 
 
 class DispatchBuffers(NamedTuple):
-    out: torch.Tensor             # [max_rows, H] bfloat16 or uint8 (E4M3 codes)
-    out_scales: Optional[torch.Tensor]  # [max_rows, H/128] float32 (FP8 only)
+    out: torch.Tensor             # [max_rows, H] bfloat16, uint8 (E4M3 codes) or int8
+    out_scales: Optional[torch.Tensor]  # float32 [max_rows, H/128] (FP8), [max_rows] (a scale a row)
     expert_counts: torch.Tensor   # [E] int32
     expert_offsets: torch.Tensor  # [E+1] int32; [E] = rows used
     group_offsets: torch.Tensor   # [groups+1] int32
@@ -406,6 +420,120 @@ def moe_dispatch_no_alloc(x: torch.Tensor, topk_idx: torch.Tensor, E: int, group
             _ptr(bufs.expert_offsets), _ptr(bufs.group_offsets), _ptr(bufs.row_src),
             _ptr(bufs.dst_row), _stream(dev)))
     return bufs
+
+
+def alloc_dispatch_quantized(T: int, H: int, E: int, k: int, groups: int = 1, row_align: int = 1,
+                             dtype=torch.int8, scales: Optional[int] = None,
+                             device="cuda") -> DispatchBuffers:
+    """Capacity-sized output buffers and workspace for moe_dispatch_quantized:
+    rows of H bytes of `dtype` (torch.int8 or torch.uint8) and their scales,
+    float32 [max_rows] (scales None) or [max_rows, scales]."""
+    dev = torch.device(device)
+    R = moe_dispatch_max_rows(T, E, k, row_align)
+    i32 = dict(dtype=torch.int32, device=dev)
+    return DispatchBuffers(
+        out=torch.empty((R, H), dtype=dtype, device=dev),
+        out_scales=torch.empty((R,) if scales is None else (R, scales), dtype=torch.float32,
+                               device=dev),
+        expert_counts=torch.empty(E, **i32), expert_offsets=torch.empty(E + 1, **i32),
+        group_offsets=torch.empty(groups + 1, **i32), row_src=torch.empty(R, **i32),
+        dst_row=torch.empty((T, k), **i32),
+        workspace=torch.empty(max(moe_dispatch_workspace_bytes(T, E, k, groups), 16),
+                              dtype=torch.uint8, device=dev))
+
+
+def moe_dispatch_quantized(x: torch.Tensor, x_scales: torch.Tensor, topk_idx: torch.Tensor, E: int,
+                           groups: int = 1, row_align: int = 1,
+                           bufs: Optional[DispatchBuffers] = None) -> DispatchBuffers:
+    """Stable per-expert scatter of rows already in 8 bits, codes and scales as
+    they are: x int8 or uint8 [T,H], x_scales float32 [T] (a scale a token) or
+    [T,S] (1x128 blocks: S = H/128); out_scales is [max_rows] or [max_rows,S]."""
+    if x.dtype not in (torch.int8, torch.uint8):
+        raise TypeError(f"x: dtype {x.dtype}, expected int8 or uint8")
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected (T, H)")
+    _need(x, "x", x.dtype)
+    T, H = x.shape
+    dev = x.device
+    _need(x_scales, "x_scales", torch.float32, None, dev)
+    if x_scales.dim() not in (1, 2) or x_scales.shape[0] != T:
+        raise ValueError(f"x_scales: shape {tuple(x_scales.shape)}, expected ({T},) or ({T}, S)")
+    tail = tuple(x_scales.shape[1:])
+    _need(topk_idx, "topk_idx", torch.int32, None, dev)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError(f"topk_idx: shape {tuple(topk_idx.shape)}, expected ({T}, k)")
+    k = topk_idx.shape[1]
+    if bufs is None:
+        bufs = alloc_dispatch_quantized(T, H, E, k, groups, row_align, x.dtype,
+                                        tail[0] if tail else None, dev)
+    R = moe_dispatch_max_rows(T, E, k, row_align)
+    _need(bufs.out, "out", x.dtype, (R, H), dev)
+    _need(bufs.out_scales, "out_scales", torch.float32, (R,) + tail, dev)
+    _need(bufs.expert_counts, "expert_counts", torch.int32, (E,), dev)
+    _need(bufs.expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev)
+    _need(bufs.group_offsets, "group_offsets", torch.int32, (groups + 1,), dev)
+    _need(bufs.row_src, "row_src", torch.int32, (R,), dev)
+    _need(bufs.dst_row, "dst_row", torch.int32, (T, k), dev)
+    _need(bufs.workspace, "workspace", torch.uint8, None, dev)
+    _run("moe_dispatch_quantized", dev, x.data_ptr(), x_scales.data_ptr(), topk_idx.data_ptr(), T,
+         H, tail[0] if tail else 1, E, k, groups, row_align, bufs.out.data_ptr(),
+         bufs.out_scales.data_ptr(), bufs.expert_counts.data_ptr(), bufs.expert_offsets.data_ptr(),
+         bufs.group_offsets.data_ptr(), bufs.row_src.data_ptr(), bufs.dst_row.data_ptr(),
+         bufs.workspace.data_ptr(), bufs.workspace.numel())
+    return bufs
+
+
+# ----------------------------------------------------------------- norm
+
+def moe_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor,
+                      residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      quant: str = "int8", with_y: bool = False,
+                      sum_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None,
+                      out_scales: Optional[torch.Tensor] = None):
+    """h = x + residual, v = h weight / sqrt(mean(h^2) + eps), v in 8 bits:
+    (out, out_scales, y, sum). quant "int8": out int8 [T,H], out_scales float32
+    [T], the operands of moe_dispatch_quantized and moe_grouped_gemm_int8;
+    "fp8": out uint8 E4M3 codes, out_scales [T, H/128]. y = bf16(v), written if
+    given or asked for by with_y (else None); sum = bf16(h), the next residual,
+    None without one; sum_out may be the residual itself. x: bfloat16 [T,H],
+    rows may be strided; weight: bfloat16 [H]."""
+    if x.dtype is not torch.bfloat16:
+        raise TypeError(f"x: dtype {x.dtype}, expected bfloat16")
+    if not x.is_cuda:
+        raise TypeError("x: must be a GPU tensor")
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected (T, H)")
+    T, H = x.shape
+    ld = x.stride(0)
+    if T <= 1:      # a single row has no row stride (torch may report any)
+        ld = H
+    if (H > 1 and x.stride(1) != 1) or ld < H:
+        raise ValueError(f"x: strides {x.stride()}, expected (>= H, 1)")
+    dev = x.device
+    _need(weight, "weight", torch.bfloat16, (H,), dev)
+    fp8 = _choice(MOE_QUANTS, quant, "quant")
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, (T, H), dev)
+        if sum_out is None:
+            sum_out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    if sum_out is not None:
+        _need(sum_out, "sum_out", torch.bfloat16, (T, H), dev)
+    if y is None and with_y:
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    if y is not None:
+        _need(y, "y", torch.bfloat16, (T, H), dev)
+    codes = torch.uint8 if fp8 else torch.int8
+    if out is None:
+        out = torch.empty((T, H), dtype=codes, device=dev)
+    _need(out, "out", codes, (T, H), dev)
+    sc_shape = (T, H // 128) if fp8 else (T,)
+    if out_scales is None:
+        out_scales = torch.empty(sc_shape, dtype=torch.float32, device=dev)
+    _need(out_scales, "out_scales", torch.float32, sc_shape, dev)
+    _run("moe_rmsnorm_quant", dev, x.data_ptr(), ld, _addr(residual), weight.data_ptr(), T, H,
+         eps, fp8, _addr(sum_out), _addr(y), out.data_ptr(), out_scales.data_ptr())
+    return out, out_scales, y, sum_out
 
 
 # ----------------------------------------------------------------- combine
@@ -561,7 +689,45 @@ def moe_grouped_gemm_bf16(a: torch.Tensor, expert_offsets: torch.Tensor, w: torc
     return y
 
 
-# ----------------------------------------------------------------- between the FP8 products
+def moe_grouped_gemm_int8(a: torch.Tensor, a_scales: torch.Tensor, expert_offsets: torch.Tensor,
+                          w: torch.Tensor, w_scales: torch.Tensor,
+                          bias: Optional[torch.Tensor] = None, act: str = "none",
+                          gated: bool = False, residual: Optional[torch.Tensor] = None,
+                          y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """INT8 grouped GEMM over segments of quantised rows with its epilogue: with
+    z = (a w[e]^T) a_scales w_scales[e] + bias[e], y = act(z) + residual
+    [max_rows, N], or gated y = act(z[:, :N/2]) * z[:, N/2:] + residual
+    [max_rows, N/2], bfloat16. Rows of no segment are left as they were.
+    a: int8 [max_rows, K], a_scales: float32 [max_rows], w: int8 [E, N, K],
+    w_scales: float32 [E, N], bias: bfloat16 [E, N]; residual may be y itself."""
+    _need(a, "a", torch.int8)
+    dev = a.device
+    _need(w, "w", torch.int8, None, dev)
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError(f"a, w: shapes {tuple(a.shape)}, {tuple(w.shape)}, "
+                         "expected (max_rows, K), (E, N, K)")
+    R, K = a.shape
+    E, N, Kw = w.shape
+    if Kw != K:
+        raise ValueError(f"w: inner size {Kw}, expected {K}")
+    n_out = N // 2 if gated else N
+    _need(a_scales, "a_scales", torch.float32, (R,), dev)
+    _need(w_scales, "w_scales", torch.float32, (E, N), dev)
+    _need(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev)
+    if bias is not None:
+        _need(bias, "bias", torch.bfloat16, (E, N), dev)
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, (R, n_out), dev)
+    if y is None:
+        y = torch.empty((R, n_out), dtype=torch.bfloat16, device=dev)
+    _need(y, "y", torch.bfloat16, (R, n_out), dev)
+    _run("moe_grouped_gemm_int8", dev, a.data_ptr(), a_scales.data_ptr(),
+         expert_offsets.data_ptr(), w.data_ptr(), w_scales.data_ptr(), _addr(bias),
+         _addr(residual), E, N, K, R, _choice(MOE_ACTS, act, "act"), int(gated), y.data_ptr())
+    return y
+
+
+# ----------------------------------------------------------------- between the products
 
 def moe_gated_act_quant_fp8(h: torch.Tensor, expert_offsets: torch.Tensor, act: str = "silu",
                             out: Optional[torch.Tensor] = None,
@@ -583,6 +749,31 @@ def moe_gated_act_quant_fp8(h: torch.Tensor, expert_offsets: torch.Tensor, act: 
     _need(out, "out", torch.uint8, (R, I), dev)
     _need(out_scales, "out_scales", torch.float32, (R, I // 128), dev)
     _run("moe_gated_act_quant_fp8", dev, h.data_ptr(), expert_offsets.data_ptr(),
+         expert_offsets.numel() - 1, R, I, _choice(MOE_ACTS, act, "act"), out.data_ptr(),
+         out_scales.data_ptr())
+    return out, out_scales
+
+
+def moe_gated_act_quant_int8(h: torch.Tensor, expert_offsets: torch.Tensor, act: str = "silu",
+                             out: Optional[torch.Tensor] = None,
+                             out_scales: Optional[torch.Tensor] = None):
+    """act(h[:, :I]) * h[:, I:] of the rows below expert_offsets[E], quantised
+    with one scale a row: (out int8 [max_rows, I], out_scales float32
+    [max_rows]), the operands of the next moe_grouped_gemm_int8. h: bfloat16
+    [max_rows, 2I]. Rows behind the last segment are left as they were."""
+    _need(h, "h", torch.bfloat16)
+    dev = h.device
+    if h.dim() != 2 or h.shape[1] % 2:
+        raise ValueError(f"h: shape {tuple(h.shape)}, expected (max_rows, 2 I)")
+    R, I = h.shape[0], h.shape[1] // 2
+    _need(expert_offsets, "expert_offsets", torch.int32, None, dev)
+    if out is None:
+        out = torch.empty((R, I), dtype=torch.int8, device=dev)
+    if out_scales is None:
+        out_scales = torch.empty((R,), dtype=torch.float32, device=dev)
+    _need(out, "out", torch.int8, (R, I), dev)
+    _need(out_scales, "out_scales", torch.float32, (R,), dev)
+    _run("moe_gated_act_quant_int8", dev, h.data_ptr(), expert_offsets.data_ptr(),
          expert_offsets.numel() - 1, R, I, _choice(MOE_ACTS, act, "act"), out.data_ptr(),
          out_scales.data_ptr())
     return out, out_scales

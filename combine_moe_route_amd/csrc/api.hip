@@ -22,6 +22,23 @@ bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
     return a < b ? b - a < (uint64_t)n : a - b < (uint64_t)m;
 }
 
+struct Range {
+    const void* p;
+    int64_t n;
+};
+
+// An output shares a byte with an input or with another output (empty ranges do not).
+bool any_overlap(const Range* in, int n_in, const Range* out, int n_out) {
+    for (int i = 0; i < n_out; i++) {
+        if (out[i].n <= 0) continue;
+        for (int j = 0; j < n_in; j++)
+            if (in[j].n > 0 && overlap(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
+        for (int j = 0; j < i; j++)
+            if (out[j].n > 0 && overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+    }
+    return false;
+}
+
 // Byte range [p, p + n) shares a byte with one of `rows` rows of `width` bytes,
 // the first at q, `step` bytes apart (step >= width). The last row that starts
 // before p + n is the only one that has to be looked at.
@@ -133,13 +150,14 @@ namespace {
 // (MOE_ENULL), alignment (MOE_EALIGN) and the workspace size (MOE_ENOSPC);
 // nothing is launched unless every check passes. With library_ws the
 // workspace is the library's own scratch (only its size is checked); with
-// run == false the checks run and nothing is launched.
+// run == false the checks run and nothing is launched. With scales > 0 the rows
+// are H bytes that are copied as they are, with that many scales each.
 int dispatch_impl(const float* logits, float* topk_w, const void* x, const int32_t* topk_idx,
                   int64_t T, int H, int E, int k, int groups, int row_align, int out_dtype,
                   void* out, float* out_scales, int32_t* expert_counts, int32_t* expert_offsets,
                   int32_t* group_offsets, int32_t* row_src, int32_t* dst_row, void* workspace,
                   size_t workspace_bytes, hipStream_t stream, bool library_ws = false,
-                  bool run = true) {
+                  bool run = true, const float* x_scales = nullptr, int scales = 0) {
     const bool route = logits != nullptr || topk_w != nullptr;   // moe_route_dispatch
     // sizes and options
     const int64_t max_rows = max_rows_of(T, E, k, row_align);
@@ -163,6 +181,9 @@ int dispatch_impl(const float* logits, float* topk_w, const void* x, const int32
     a.fp8 = fp8;
     a.out = out;
     a.out_scales = out_scales;
+    a.x_scales = x_scales;
+    a.scales = scales;
+    if (scales > 0) a.H = H / 2;       // the copy counts in 2-byte units
     a.expert_counts = expert_counts;
     a.expert_offsets = expert_offsets;
     a.group_offsets = group_offsets;
@@ -184,17 +205,32 @@ int dispatch_impl(const float* logits, float* topk_w, const void* x, const int32
     if (T > 0 && (!x || !topk_idx || !dst_row)) return MOE_ENULL;
     if (route && T > 0 && (!logits || !topk_w)) return MOE_ENULL;
     if (max_rows > 0 && (!out || !row_src)) return MOE_ENULL;
-    if (fp8 && max_rows > 0 && !out_scales) return MOE_ENULL;
+    if ((fp8 || scales > 0) && max_rows > 0 && !out_scales) return MOE_ENULL;
+    if (scales > 0 && T > 0 && !x_scales) return MOE_ENULL;
     // alignment
     if (!aligned(x, 16) || !aligned(out, 16)) return MOE_EALIGN;
     if (!aligned(topk_idx, 4) || !aligned(expert_counts, 4) || !aligned(expert_offsets, 4) ||
         !aligned(group_offsets, 4) || !aligned(row_src, 4) || !aligned(dst_row, 4) ||
-        !aligned(workspace, 16) || (fp8 && !aligned(out_scales, 4)))
+        !aligned(workspace, 16) || ((fp8 || scales > 0) && !aligned(out_scales, 4)) ||
+        !aligned(x_scales, 4))
         return MOE_EALIGN;
     if (route && (!aligned(logits, 4) || !aligned(topk_w, 4))) return MOE_EALIGN;
     // workspace
     if (workspace_bytes < ws.total) return MOE_ENOSPC;
     if (!library_ws && ws.total > 0 && !workspace) return MOE_ENULL;
+    if (scales > 0) {
+        // what one kernel writes is read, or written, by other blocks of the call
+        const Range in[] = {{x, T * H}, {x_scales, T * scales * 4}, {topk_idx, T * k * 4}};
+        const Range out_r[] = {{out, max_rows * H},
+                               {out_scales, max_rows * scales * 4},
+                               {expert_counts, (int64_t)E * 4},
+                               {expert_offsets, ((int64_t)E + 1) * 4},
+                               {group_offsets, group_offsets ? ((int64_t)groups + 1) * 4 : 0},
+                               {row_src, max_rows * 4},
+                               {dst_row, T * k * 4},
+                               {workspace, (int64_t)ws.total}};
+        if (any_overlap(in, 3, out_r, 8)) return MOE_EINVAL;
+    }
     if (!run) return MOE_OK;
 
     const hipError_t e = moe::launch_dispatch(a, stream, info, &nk);
@@ -284,6 +320,19 @@ int moe_dispatch_no_alloc(const void* x, const int32_t* topk_idx, int64_t T, int
                          out, out_scales, expert_counts, expert_offsets, group_offsets, row_src,
                          dst_row, ws, MOE_NO_ALLOC_SCRATCH_BYTES,
                          static_cast<hipStream_t>(stream), /*library_ws=*/true);
+}
+
+int moe_dispatch_quantized(const void* x, const float* x_scales, const int32_t* topk_idx,
+                           int64_t T, int H, int scales, int E, int k, int groups, int row_align,
+                           void* out, float* out_scales, int32_t* expert_counts,
+                           int32_t* expert_offsets, int32_t* group_offsets, int32_t* row_src,
+                           int32_t* dst_row, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    if (H < 16 || H > 65536 || H % 16 != 0 || scales < 1 || scales > H) return MOE_EINVAL;
+    return dispatch_impl(nullptr, nullptr, x, topk_idx, T, H, E, k, groups, row_align,
+                         MOE_OUT_BF16, out, out_scales, expert_counts, expert_offsets,
+                         group_offsets, row_src, dst_row, workspace, workspace_bytes,
+                         static_cast<hipStream_t>(stream), false, true, x_scales, scales);
 }
 
 int moe_combine(const void* expert_out, const int32_t* dst_row, const float* topk_w, int64_t T,
@@ -460,7 +509,7 @@ int moe_grouped_gemm_bf16(const void* a, const int32_t* expert_offsets, const vo
     if (K < 8 || K > (1 << 20) || K % 8 != 0) return MOE_EINVAL;
     if (N < 8 || N > (1 << 20) || N % (gated ? 16 : 8) != 0) return MOE_EINVAL;
     if (act < MOE_ACT_NONE || act > MOE_ACT_GELU) return MOE_EINVAL;
-    moe::GemmBf16Args g;
+    moe::GroupedGemmArgs g = {};
     g.a = static_cast<const uint16_t*>(a);
     g.off = expert_offsets;
     g.w = static_cast<const uint16_t*>(w);
@@ -489,6 +538,128 @@ int moe_grouped_gemm_bf16(const void* a, const int32_t* expert_offsets, const vo
         (residual && residual != y && overlap(y, y_bytes, residual, y_bytes)))
         return MOE_EINVAL;
     const hipError_t e = moe::launch_grouped_gemm_bf16(g, static_cast<hipStream_t>(stream), &info);
+    if (log_enabled()) log_launch(info.name, info);
+    return status_of(e);
+}
+
+int moe_grouped_gemm_int8(const void* a, const float* a_scales, const int32_t* expert_offsets,
+                          const void* w, const float* w_scales, const void* bias,
+                          const void* residual, int E, int N, int K, int64_t max_rows, int act,
+                          int gated, void* y, void* stream) {
+    if (E < 1 || E > MOE_MAX_EXPERTS || max_rows < 0 || max_rows > kInt32Max) return MOE_EINVAL;
+    // K (-128)^2 < 2^31: the whole-number sums fit 32 bits
+    if (K < 16 || K > (1 << 17) - 16 || K % 16 != 0) return MOE_EINVAL;
+    if (N < 8 || N > (1 << 20) || N % (gated ? 16 : 8) != 0) return MOE_EINVAL;
+    if (act < MOE_ACT_NONE || act > MOE_ACT_GELU) return MOE_EINVAL;
+    moe::GroupedGemmArgs g = {};
+    g.a = static_cast<const uint16_t*>(a);
+    g.off = expert_offsets;
+    g.w = static_cast<const uint16_t*>(w);
+    g.bias = static_cast<const uint16_t*>(bias);
+    g.residual = static_cast<const uint16_t*>(residual);
+    g.y = static_cast<uint16_t*>(y);
+    g.a_scales = a_scales;
+    g.w_scales = w_scales;
+    g.max_rows = max_rows;
+    g.E = E;
+    g.N = N;
+    g.K = K / 2;                       // pairs of values
+    g.act = act;
+    g.gated = gated != 0;
+    moe::LaunchInfo info;
+    (void)moe::launch_grouped_gemm_int8(g, nullptr, &info, false);
+    if (!all_fit(&info, 1)) return MOE_EINVAL;
+    if (max_rows == 0) return MOE_OK;
+    if (!a || !a_scales || !expert_offsets || !w || !w_scales || !y) return MOE_ENULL;
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(bias, 16) ||
+        !aligned(residual, 16) || !aligned(w_scales, 16) || !aligned(a_scales, 4) ||
+        !aligned(expert_offsets, 4))
+        return MOE_EALIGN;
+    // a workgroup writes y while others still read the operands
+    const Range out = {y, max_rows * (gated ? N / 2 : N) * 2};
+    const Range in[] = {{a, max_rows * K},
+                        {a_scales, max_rows * 4},
+                        {expert_offsets, ((int64_t)E + 1) * 4},
+                        {w, (int64_t)E * N * K},
+                        {w_scales, (int64_t)E * N * 4},
+                        {bias, bias ? (int64_t)E * N * 2 : 0},
+                        {residual, residual && residual != y ? out.n : 0}};
+    if (any_overlap(in, 7, &out, 1)) return MOE_EINVAL;
+    const hipError_t e = moe::launch_grouped_gemm_int8(g, static_cast<hipStream_t>(stream), &info);
+    if (log_enabled()) log_launch(info.name, info);
+    return status_of(e);
+}
+
+int moe_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual, const void* weight,
+                      int64_t T, int H, float eps, int quant, void* sum, void* y, void* out,
+                      float* out_scales, void* stream) {
+    if (T < 0 || T > kInt32Max) return MOE_EINVAL;
+    if (quant != MOE_QUANT_INT8 && quant != MOE_QUANT_FP8_E4M3) return MOE_EINVAL;
+    const bool fp8 = quant == MOE_QUANT_FP8_E4M3;
+    if (H < 8 || H > 65536 || H % (fp8 ? 128 : 8) != 0) return MOE_EINVAL;
+    if (ld_x < H || ld_x % 8 != 0 || ld_x > ((int64_t)1 << 31) || T * ld_x > ((int64_t)1 << 40))
+        return MOE_EINVAL;
+    if (!(eps >= 1e-30f && eps <= 1.0f)) return MOE_EINVAL;
+    if (sum && !residual) return MOE_EINVAL;
+    moe::NormArgs a;
+    a.x = static_cast<const uint16_t*>(x);
+    a.residual = static_cast<const uint16_t*>(residual);
+    a.weight = static_cast<const uint16_t*>(weight);
+    a.sum = static_cast<uint16_t*>(sum);
+    a.y = static_cast<uint16_t*>(y);
+    a.out = static_cast<uint8_t*>(out);
+    a.scales = out_scales;
+    a.T = T;
+    a.ld = ld_x;
+    a.H = H;
+    a.eps = eps;
+    a.fp8 = fp8;
+    moe::LaunchInfo info;
+    (void)moe::launch_rmsnorm_quant(a, nullptr, &info, false);
+    if (!all_fit(&info, 1)) return MOE_EINVAL;
+    if (T == 0) return MOE_OK;
+    if (!x || !weight || !out || !out_scales) return MOE_ENULL;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum, 16) ||
+        !aligned(y, 16) || !aligned(out, fp8 ? 16 : 8) || !aligned(out_scales, 4))
+        return MOE_EALIGN;
+    // rows are written while others are still read; sum may be the residual itself
+    const int64_t rows = T * H * 2;
+    const Range outs[] = {{sum, sum && sum != residual ? rows : 0},
+                          {y, y ? rows : 0},
+                          {out, T * H},
+                          {out_scales, T * (fp8 ? H / 128 : 1) * 4}};
+    const Range in[] = {{residual, residual ? rows : 0}, {weight, (int64_t)H * 2}};
+    if (any_overlap(in, 2, outs, 4)) return MOE_EINVAL;
+    if (sum && sum == residual && overlap(sum, rows, weight, (int64_t)H * 2)) return MOE_EINVAL;
+    const Range all[] = {{sum, sum ? rows : 0}, outs[1], outs[2], outs[3]};
+    for (const Range& o : all)
+        if (o.n > 0 && overlap_rows(o.p, o.n, x, T, ld_x * 2, (int64_t)H * 2)) return MOE_EINVAL;
+    const hipError_t e = moe::launch_rmsnorm_quant(a, static_cast<hipStream_t>(stream), &info);
+    if (log_enabled()) log_launch(info.name, info);
+    return status_of(e);
+}
+
+int moe_gated_act_quant_int8(const void* h, const int32_t* expert_offsets, int E, int64_t max_rows,
+                             int I, int act, void* out, float* out_scales, void* stream) {
+    if (E < 1 || E > MOE_MAX_EXPERTS || max_rows < 0 || max_rows > kInt32Max) return MOE_EINVAL;
+    if (I < 16 || I > 32768 || I % 16 != 0) return MOE_EINVAL;
+    if (act < MOE_ACT_NONE || act > MOE_ACT_GELU) return MOE_EINVAL;
+    moe::LaunchInfo info;
+    (void)moe::launch_gated_act_int8(h, expert_offsets, E, max_rows, I, act, out, out_scales,
+                                     nullptr, &info, false);
+    if (!all_fit(&info, 1)) return MOE_EINVAL;
+    if (max_rows == 0) return MOE_OK;
+    if (!h || !expert_offsets || !out || !out_scales) return MOE_ENULL;
+    if (!aligned(h, 16) || !aligned(out, 16) || !aligned(out_scales, 4) ||
+        !aligned(expert_offsets, 4))
+        return MOE_EALIGN;
+    // workgroups write out while others still read h and the number of rows
+    const Range in[] = {{h, max_rows * I * 4}, {expert_offsets, ((int64_t)E + 1) * 4}};
+    const Range outs[] = {{out, max_rows * I}, {out_scales, max_rows * 4}};
+    if (any_overlap(in, 2, outs, 2)) return MOE_EINVAL;
+    const hipError_t e = moe::launch_gated_act_int8(h, expert_offsets, E, max_rows, I, act, out,
+                                                    out_scales, static_cast<hipStream_t>(stream),
+                                                    &info);
     if (log_enabled()) log_launch(info.name, info);
     return status_of(e);
 }

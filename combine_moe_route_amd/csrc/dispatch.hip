@@ -537,8 +537,9 @@ constexpr int kScatterThreads = 256;
 // Zero the pad rows of one expert's segment, or the part of them this
 // block owns (pad rows of expert e: [offsets[e] + counts[e], offsets[e+1])).
 // Rows outside [0, max_rows) are never written, whatever the offsets say.
-__device__ void zero_pad_rows(int pb, int pad_blocks_per_expert, int pad_rows_per_block, int H,
-                              bool fp8, int64_t max_rows,
+// A row has `row_bytes` bytes and `nb` scales.
+__device__ void zero_pad_rows(int pb, int pad_blocks_per_expert, int pad_rows_per_block,
+                              int row_bytes, int nb, int64_t max_rows,
                               const int32_t* __restrict__ expert_counts,
                               const int32_t* __restrict__ expert_offsets,
                               unsigned char* __restrict__ out, float* __restrict__ scales,
@@ -551,8 +552,7 @@ __device__ void zero_pad_rows(int pb, int pad_blocks_per_expert, int pad_rows_pe
     const int hi = (int)min(npad, (int64_t)lo + pad_rows_per_block);
     if (first < 0 || lo >= hi) return;
     const int rows = hi - lo;
-    const int64_t row_bytes = fp8 ? (int64_t)H : 2 * (int64_t)H;
-    const int units = (int)(row_bytes / 16);
+    const int units = row_bytes / 16;
     const int64_t r0 = (int64_t)first + lo;
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
     for (int u = threadIdx.x; u < rows * units; u += blockDim.x) {
@@ -560,10 +560,7 @@ __device__ void zero_pad_rows(int pb, int pad_blocks_per_expert, int pad_rows_pe
         const int c = u - rr * units;
         *reinterpret_cast<uint4*>(out + (r0 + rr) * row_bytes + 16 * (int64_t)c) = z;
     }
-    if (fp8) {
-        const int nb = H / 128;
-        for (int i = threadIdx.x; i < rows * nb; i += blockDim.x) scales[r0 * nb + i] = 0.0f;
-    }
+    for (int i = threadIdx.x; i < rows * nb; i += blockDim.x) scales[r0 * nb + i] = 0.0f;
     for (int i = threadIdx.x; i < rows; i += blockDim.x) row_src[r0 + i] = -1;
 }
 
@@ -656,11 +653,6 @@ __device__ __forceinline__ void publish_rows(int lane, int64_t p0, int j0, int k
     }
 }
 
-// bf16 rows. One wave per (token, chunk of 64 lane units of 8 bf16 = 16
-// bytes). The token index is wave-uniform, so its expert ids, in-tile ranks
-// and tile bases come in through scalar loads; the x row is read once through
-// a range descriptor (lanes past the row read zeros) and stored to each of the
-// token's rows.
 // Scan outputs as the scatter reads them: offsets [E+1], counts [E] and tile
 // prefixes [tiles, E], from global memory (scan kernel) or from LDS (inline).
 struct ScanView {
@@ -683,8 +675,21 @@ struct RouteArgs {
     float* topk_w;
 };
 
-template <int MODE, int KL>
-__global__ __launch_bounds__(kScatterThreads) void k_scatter_bf16(
+// Scales that travel with rows that are already quantised: S of a token, copied
+// to each of its rows.
+struct RowScales {
+    const float* x;   // [T, S]
+    float* out;       // [max_rows, S]
+    int S;
+};
+
+// Rows as they are: bf16, or (SCALED) 8-bit codes counted as H 2-byte units, with
+// S scales a token. One wave per (token, chunk of 64 lane units of 16 bytes). The
+// token index is wave-uniform, so its expert ids, in-tile ranks and tile bases come
+// in through scalar loads; the x row is read once through a range descriptor (lanes
+// past the row read zeros) and stored to each of the token's rows.
+template <int MODE, int KL, bool SCALED>
+__global__ __launch_bounds__(kScatterThreads) void k_scatter_rows(
     const uint16_t* __restrict__ x, const int32_t* __restrict__ topk_idx,
     const uint8_t* __restrict__ tile_rank, const int32_t* __restrict__ tile_base,
     const uint8_t* __restrict__ tile_counts, int tiles, int row_align, int groups,
@@ -692,7 +697,7 @@ __global__ __launch_bounds__(kScatterThreads) void k_scatter_bf16(
     int32_t* __restrict__ expert_counts, int32_t* __restrict__ expert_offsets,
     int64_t T, int H, int E, int k, int TT, int64_t max_rows, int pad_blocks,
     int pad_blocks_per_expert, int pad_rows_per_block, unsigned char* __restrict__ out,
-    int32_t* __restrict__ row_src, int32_t* __restrict__ dst_row, RouteArgs ra) {
+    int32_t* __restrict__ row_src, int32_t* __restrict__ dst_row, RouteArgs ra, RowScales rs) {
     const int lane = threadIdx.x & (kWave - 1);
     const int U = H / 8;                           // 16-byte units per row
     const int CW = (U + kWave - 1) / kWave;        // waves per token
@@ -729,8 +734,8 @@ __global__ __launch_bounds__(kScatterThreads) void k_scatter_bf16(
         sv = ScanView{Ls.off, Ls.cnt, nullptr};
     }
     if (pad_block) {
-        zero_pad_rows(blockIdx.x, pad_blocks_per_expert, pad_rows_per_block, H, false, max_rows,
-                      sv.cnt, sv.off, out, nullptr, row_src);
+        zero_pad_rows(blockIdx.x, pad_blocks_per_expert, pad_rows_per_block, 2 * H,
+                      SCALED ? rs.S : 0, max_rows, sv.cnt, sv.off, out, rs.out, row_src);
         return;
     }
     if (t >= T) return;
@@ -761,6 +766,14 @@ __global__ __launch_bounds__(kScatterThreads) void k_scatter_bf16(
             for (int jj = 0; jj < 8; jj++)
                 if (r[jj] >= 0)
                     *reinterpret_cast<uint4*>(out + (int64_t)r[jj] * 2 * H + 16 * (int64_t)u) = a;
+        }
+        if (SCALED && chunk == 0) {
+            for (int i = lane; i < rs.S; i += kWave) {
+                const float s = rs.x[t * rs.S + i];
+#pragma unroll
+                for (int jj = 0; jj < 8; jj++)
+                    if (r[jj] >= 0) rs.out[(int64_t)r[jj] * rs.S + i] = s;
+            }
         }
     }
 }
@@ -835,8 +848,8 @@ __global__ __launch_bounds__(1024) void k_scatter_fp8(
         sv = ScanView{Ls.off, Ls.cnt, nullptr};
     }
     if (pad_block) {
-        zero_pad_rows((int)(-1 - role), pad_blocks_per_expert, pad_rows_per_block, H, true, max_rows,
-                      sv.cnt, sv.off, out, scales, row_src);
+        zero_pad_rows((int)(-1 - role), pad_blocks_per_expert, pad_rows_per_block, H, H / 128,
+                      max_rows, sv.cnt, sv.off, out, scales, row_src);
         return;
     }
     const int64_t p0 = t * k;
@@ -1044,14 +1057,18 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t stream, LaunchInfo
             a.max_rows, (int)pad_blocks, pad_per_expert, pad_rows_per_block, out, a.out_scales,
             a.row_src, a.dst_row, ra);
     } else {
-        auto kern = routed ? (kl == 2 ? k_scatter_bf16<kRouted, 2>
-                              : kl == 4 ? k_scatter_bf16<kRouted, 4> : k_scatter_bf16<kRouted, 8>)
-                    : inline_scan_ok ? k_scatter_bf16<kInline, 2> : k_scatter_bf16<kScanned, 2>;
+        auto kern = a.scales > 0 ? (inline_scan_ok ? k_scatter_rows<kInline, 2, true>
+                                                   : k_scatter_rows<kScanned, 2, true>)
+                    : routed ? (kl == 2   ? k_scatter_rows<kRouted, 2, false>
+                                : kl == 4 ? k_scatter_rows<kRouted, 4, false>
+                                          : k_scatter_rows<kRouted, 8, false>)
+                    : inline_scan_ok ? k_scatter_rows<kInline, 2, false>
+                                     : k_scatter_rows<kScanned, 2, false>;
         kern<<<dim3((unsigned)scatter_blocks), dim3(kScatterThreads), 0, stream>>>(
             x, a.topk_idx, a.tile_rank, a.tile_base, a.tile_counts, (int)tiles, a.row_align,
             a.groups, a.group_offsets, a.expert_counts, a.expert_offsets, a.T, a.H, a.E, a.k, TT,
             a.max_rows, (int)pad_blocks, pad_per_expert, pad_rows_per_block, out, a.row_src,
-            a.dst_row, ra);
+            a.dst_row, ra, RowScales{a.x_scales, a.out_scales, a.scales});
     }
     return hipGetLastError();
 }

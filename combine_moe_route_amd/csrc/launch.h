@@ -56,6 +56,9 @@ struct DispatchArgs {
     int32_t* tile_base;     // workspace [tiles, E]
     uint8_t* tile_rank;     // workspace [T, k]
     int64_t max_rows;       // rows in out / out_scales / row_src
+    // moe_dispatch_quantized: x and out are rows of 2 H bytes with `scales` scales each
+    const float* x_scales = nullptr;   // [T, scales]
+    int scales = 0;
 };
 
 // Tokens per count tile (16, 32 or 64, growing with T; at most 64, so tile
@@ -122,20 +125,47 @@ struct ScoredArgs {
 hipError_t launch_route_scored(const ScoredArgs& a, hipStream_t stream, LaunchInfo* info,
                                bool run = true);
 
-// bf16 grouped GEMM with its epilogue (moe_grouped_gemm_bf16).
-struct GemmBf16Args {
+// Grouped GEMMs with an epilogue (moe_grouped_gemm_bf16, moe_grouped_gemm_int8).
+// Operand rows are K 2-byte units: bf16 values, or pairs of int8 values.
+struct GroupedGemmArgs {
     const uint16_t* a;
     const int32_t* off;
     const uint16_t* w;
     const uint16_t* bias;        // [E, N] or nullptr
     const uint16_t* residual;    // [max_rows, N or N/2] or nullptr
     uint16_t* y;
+    const float* a_scales;       // int8: [max_rows]
+    const float* w_scales;       // int8: [E, N]
     int64_t max_rows;
     int E, N, K, act;
     bool gated;
 };
-hipError_t launch_grouped_gemm_bf16(const GemmBf16Args& g, hipStream_t stream, LaunchInfo* info,
+hipError_t launch_grouped_gemm_bf16(const GroupedGemmArgs& g, hipStream_t stream, LaunchInfo* info,
                                     bool run = true);
+hipError_t launch_grouped_gemm_int8(const GroupedGemmArgs& g, hipStream_t stream, LaunchInfo* info,
+                                    bool run = true);
+
+// Residual, root-mean-square norm and 8-bit output (moe_rmsnorm_quant).
+struct NormArgs {
+    const uint16_t* x;           // rows ld apart
+    const uint16_t* residual;    // or nullptr
+    const uint16_t* weight;
+    uint16_t* sum;               // or nullptr
+    uint16_t* y;                 // or nullptr
+    uint8_t* out;
+    float* scales;
+    int64_t T, ld;
+    int H;
+    float eps;
+    bool fp8;
+};
+hipError_t launch_rmsnorm_quant(const NormArgs& a, hipStream_t stream, LaunchInfo* info,
+                                bool run = true);
+
+// Gated activation with INT8 quantisation (moe_gated_act_quant_int8).
+hipError_t launch_gated_act_int8(const void* h, const int32_t* expert_offsets, int E,
+                                 int64_t max_rows, int I, int act, void* out, float* out_scales,
+                                 hipStream_t stream, LaunchInfo* info, bool run = true);
 
 // Gated activation with FP8 quantisation (moe_gated_act_quant_fp8).
 hipError_t launch_gated_act_fp8(const void* h, const int32_t* expert_offsets, int E,

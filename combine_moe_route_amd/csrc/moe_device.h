@@ -57,6 +57,19 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t w, int sel) {
     }
 }
 
+// ------------------------------------------------------------------ int8
+
+// Four fp32 values of magnitude up to 127.4 to four int8 codes (byte i = value i),
+// nearest even: adding 1.5 2^23 leaves the whole number in the lowest bits.
+__device__ __forceinline__ uint32_t f32x4_to_int8(float a, float b, float c, float d) {
+    constexpr float kMagic = 12582912.0f;
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(b + kMagic),
+                                              __float_as_uint(a + kMagic), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(d + kMagic),
+                                              __float_as_uint(c + kMagic), 0x04000c0cu);
+    return lo | hi;
+}
+
 // ------------------------------------------------------------------ DPP
 
 // DPP controls (GCN/CDNA encoding).

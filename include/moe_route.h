@@ -272,6 +272,66 @@ int moe_dispatch_no_alloc(const void* x, const int32_t* topk_idx,
                           void* stream);
 
 /*
+ * Dispatch of rows that are already in 8 bits, with their scales: what
+ * moe_rmsnorm_quant writes, or any codes of one byte. The layout, the tables and
+ * the order are moe_dispatch's; each row's H bytes and its scales are copied
+ * unchanged, pad rows get zero bytes and zero scales.
+ *
+ *   x              device [T, H] bytes, 16-byte aligned
+ *   x_scales       device fp32 [T, scales]
+ *   H              16 <= H <= 65536, H % 16 == 0
+ *   scales         scales of a row: 1 (a scale a token) or H / 128 (1x128
+ *                  blocks), or any other number from 1 to H
+ *   out            device [max_rows, H] bytes out, 16-byte aligned
+ *   out_scales     device fp32 [max_rows, scales] out
+ *   other arguments, limits and outputs as for moe_dispatch (launch limit:
+ *   64 * T * ceil(H / 1024) < 2^32). No output overlaps x, x_scales, topk_idx,
+ *   the workspace or another output (MOE_EINVAL).
+ */
+int moe_dispatch_quantized(const void* x, const float* x_scales, const int32_t* topk_idx,
+                           int64_t T, int H, int scales, int E, int k, int groups, int row_align,
+                           void* out, float* out_scales, int32_t* expert_counts,
+                           int32_t* expert_offsets, int32_t* group_offsets, int32_t* row_src,
+                           int32_t* dst_row, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * The norm in front of an expert layer: residual, root-mean-square norm, 8 bits.
+ * For every token, in fp32 (v is never rounded to bf16 on its way to the codes):
+ *
+ *   h = x[t] + residual[t]                      sum[t] = bf16(h)
+ *   v = h * weight / sqrt(mean(h^2) + eps)      y[t]   = bf16(v)
+ *   int8  s = max |v| / 127 over the token;  codes 127 v / max |v| to the nearest
+ *         whole number, even at ties: -127 .. 127
+ *   fp8   s = max |v| / 448 over 128 channels;  E4M3 codes of 448 v / max |v|,
+ *         nearest even (moe_dispatch's quantisation)
+ * A token or block whose s is 0 gets zero codes.
+ *
+ *   x            device bf16, rows ld_x elements apart (>= H, % 8 == 0), 16-byte
+ *                aligned
+ *   residual     device bf16 [T, H], 16-byte aligned, or NULL: h = x
+ *   weight       device bf16 [H], 16-byte aligned; finite, |weight| <= 2^60
+ *   sum          device bf16 [T, H] out, 16-byte aligned, or NULL; needs residual
+ *                and may be the residual itself (residual += x)
+ *   y            device bf16 [T, H] out, 16-byte aligned, or NULL: the input of
+ *                the router's gate, or of a bf16 layer
+ *   out          device int8 or E4M3 [T, H] out; 8-byte (int8) or 16-byte aligned
+ *   out_scales   device fp32 out: [T] (int8) or [T, H/128] (fp8)
+ *   H            8 <= H <= 65536, H % 8 == 0 (int8) or H % 128 == 0 (fp8)
+ *   eps          1e-30 <= eps <= 1
+ *   T >= 0 (T == 0 is a no-op), T * ld_x <= 2^40, ld_x <= 2^31, T * 1024 < 2^32
+ *   at most
+ * A token with an infinity or NaN in h (also one that the addition made) gets NaN
+ * in y and in its scales and zero codes. Outputs overlap neither inputs nor each
+ * other, but for sum == residual (MOE_EINVAL; the gaps between rows of x are free).
+ */
+typedef enum { MOE_QUANT_INT8 = 0, MOE_QUANT_FP8_E4M3 = 1 } moe_quant;
+
+int moe_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual, const void* weight,
+                      int64_t T, int H, float eps, int quant, void* sum, void* y, void* out,
+                      float* out_scales, void* stream);
+
+/*
  * Combine: each token's output is the weighted sum of the rows its experts
  * produced, y[t] = bf16(sum_j topk_w[t,j] * expert_out[dst_row[t,j]]),
  * accumulated in fp32 in slot order and rounded once to bf16 (nearest even).
@@ -435,6 +495,72 @@ int moe_grouped_gemm_bf16(const void* a, const int32_t* expert_offsets, const vo
  */
 int moe_gated_act_quant_fp8(const void* h, const int32_t* expert_offsets, int E, int64_t max_rows,
                             int I, int act, void* out, float* out_scales, void* stream);
+
+/*
+ * Grouped INT8 GEMM over segments of quantised rows, with one scale a row and one
+ * a channel of the weights. For every expert e and every row r in
+ * [expert_offsets[e], expert_offsets[e+1]):
+ *
+ *   z[n]  = fp32(sum_k a[r, k] * w[e, n, k]) * a_scales[r] * w_scales[e, n]
+ *           + bias[e, n]                                   (fp32)
+ *   plain:  y[r, n] = bf16( act(z[n]) + residual[r, n] ),               n < N
+ *   gated:  y[r, n] = bf16( act(z[n]) * z[N/2 + n] + residual[r, n] ),  n < N/2
+ *
+ * The sum of the products is exact (32-bit whole numbers); it is rounded to fp32
+ * once, and the result once to bf16. A row whose scale is NaN (a token that held a
+ * NaN) gives NaN, and no other row does.
+ *
+ *   a               device int8 [max_rows, K], 16-byte aligned
+ *   a_scales        device fp32 [max_rows]
+ *   expert_offsets  device int32 [E+1]: moe_dispatch_quantized's expert_offsets
+ *                   (any row_align). Segment bounds are clamped to [0, max_rows]
+ *   w               device int8 [E, N, K], K contiguous, 16-byte aligned
+ *   w_scales        device fp32 [E, N], 16-byte aligned
+ *   bias            device bf16 [E, N], 16-byte aligned, or NULL
+ *   residual        device bf16 [max_rows, N or N/2], 16-byte aligned, or NULL;
+ *                   may be y itself (y += ...), and may not overlap it otherwise
+ *   y               device bf16 [max_rows, N or N/2] out, 16-byte aligned.
+ *                   Rows of no segment are not written, and rows of a, a_scales
+ *                   or residual in no segment are not read.
+ *   E, N, K         1 <= E <= 1024; 16 <= K <= 2^17 - 16, K % 16 == 0;
+ *                   8 <= N <= 2^20, N % 8 == 0 (N % 16 == 0 when gated)
+ *   max_rows        rows of a, residual and y; 0 <= max_rows < 2^31
+ * No workspace; nothing is kept between calls. Errors: MOE_EINVAL (limits,
+ * launch size, y overlapping an operand other than residual == y), MOE_ENULL,
+ * MOE_EALIGN, MOE_EHIP. max_rows == 0 returns MOE_OK without a launch.
+ */
+int moe_grouped_gemm_int8(const void* a, const float* a_scales, const int32_t* expert_offsets,
+                          const void* w, const float* w_scales, const void* bias,
+                          const void* residual, int E, int N, int K, int64_t max_rows, int act,
+                          int gated, void* y, void* stream);
+
+/*
+ * Gated activation between two INT8 grouped GEMMs. For every row r below
+ * expert_offsets[E] (clamped to max_rows):
+ *
+ *   v[c]  = act(h[r, c]) * h[r, I + c]                    (fp32; past its range the
+ *           largest finite value of the sign)
+ *   s     = max |v| over the row / 127                    (fp32)
+ *   out   = 127 v / max |v| to the nearest whole number, even at ties:
+ *           -127 .. 127; a row whose s is 0 gets zero codes
+ *
+ *   h               device bf16 [max_rows, 2 I], 16-byte aligned, no infinities:
+ *                   the y of moe_grouped_gemm_int8 with N = 2 I (gate, then up).
+ *                   A row that holds a NaN in v gets the scale NaN and zero codes
+ *   expert_offsets  device int32 [E+1]; only [E] is read
+ *   out             device int8 [max_rows, I] out, 16-byte aligned
+ *   out_scales      device fp32 [max_rows] out
+ *   I % 16 == 0, 16 <= I <= 32768; 0 <= max_rows < 2^31; 1 <= E <= 1024; rows
+ *   above I = 8192 take a workgroup of 1024 threads each (max_rows * 1024 < 2^32)
+ * out and out_scales are the a and a_scales of the next moe_grouped_gemm_int8.
+ * Rows at or past expert_offsets[E] are neither read nor written; pad rows of a
+ * segment (zeros) give zero codes and scales. out and out_scales overlap neither
+ * each other nor h nor expert_offsets (MOE_EINVAL). max_rows == 0 returns MOE_OK
+ * without a launch.
+ */
+int moe_gated_act_quant_int8(const void* h, const int32_t* expert_offsets, int E,
+                             int64_t max_rows, int I, int act, void* out, float* out_scales,
+                             void* stream);
 
 /*
  * Stand-in experts for tests and the benchmark (not part of the path):
