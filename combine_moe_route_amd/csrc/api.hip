@@ -613,6 +613,7 @@ int moe_rmsnorm_quant(const void* x, int64_t ld_x, const void* residual, const v
     a.ld = ld_x;
     a.H = H;
     a.eps = eps;
+    a.inv_h = 1.0f / (float)H;
     a.fp8 = fp8;
     moe::LaunchInfo info;
     (void)moe::launch_rmsnorm_quant(a, nullptr, &info, false);

@@ -156,7 +156,7 @@ struct NormArgs {
     float* scales;
     int64_t T, ld;
     int H;
-    float eps;
+    float eps, inv_h;            // 1 / H
     bool fp8;
 };
 hipError_t launch_rmsnorm_quant(const NormArgs& a, hipStream_t stream, LaunchInfo* info,

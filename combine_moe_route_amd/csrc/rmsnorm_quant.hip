@@ -31,6 +31,18 @@ namespace {
 
 constexpr float kInf = __builtin_inff();
 
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ u32x4 load_nt(const uint16_t* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+}
+
+// Eight values times r as bf16.
+__device__ __forceinline__ uint4 bf16x8_of(const float* f, float r) {
+    return make_uint4(cvt_bf16x2(f[0] * r, f[1] * r), cvt_bf16x2(f[2] * r, f[3] * r),
+                      cvt_bf16x2(f[4] * r, f[5] * r), cvt_bf16x2(f[6] * r, f[7] * r));
+}
+
 struct FMax {
     __device__ uint32_t operator()(uint32_t a, uint32_t b) const {
         return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
@@ -77,8 +89,8 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void k_rmsnorm_quant(NormArg
         const int u = tid + i * nt;
         xv[i] = rv[i] = wv[i] = u32x4{0u, 0u, 0u, 0u};
         if (u < U) {
-            xv[i] = *reinterpret_cast<const u32x4*>(a.x + t * a.ld + 8 * u);
-            if (a.residual) rv[i] = *reinterpret_cast<const u32x4*>(a.residual + at + 8 * u);
+            xv[i] = load_nt(a.x + t * a.ld + 8 * u);
+            if (a.residual) rv[i] = load_nt(a.residual + at + 8 * u);
             wv[i] = *reinterpret_cast<const u32x4*>(a.weight + 8 * u);
         }
     }
@@ -111,9 +123,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void k_rmsnorm_quant(NormArg
         }
         const int u = tid + i * nt;
         if (a.sum && u < U)
-            *reinterpret_cast<uint4*>(a.sum + at + 8 * u) =
-                make_uint4(cvt_bf16x2(h[i][0], h[i][1]), cvt_bf16x2(h[i][2], h[i][3]),
-                           cvt_bf16x2(h[i][4], h[i][5]), cvt_bf16x2(h[i][6], h[i][7]));
+            store16_nt(a.sum + at + 8 * u, bf16x8_of(h[i], 1.0f));
     }
     measure();
     float eps = a.eps;
@@ -134,8 +144,13 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void k_rmsnorm_quant(NormArg
         measure();
     }
     const bool finite = sum < kInf;
-    const float r = finite ? 1.0f / sqrtf(sum / (float)a.H + eps) : __builtin_nanf("");
+    // the reciprocal root of the unit, with one Newton step
+    const float m = fmaf(sum, a.inv_h, eps);
+    float r = __builtin_amdgcn_rsqf(m);
+    r = fmaf(0.5f * r, fmaf(-m * r, r, 1.0f), r);
+    r = finite ? r : __builtin_nanf("");
     constexpr float kTop = FP8 ? 448.0f : 127.0f;
+    constexpr float kLeast = FP8 ? 0x1.cp-142f : 0x1.f8p-144f;   // the largest V with V / kTop == 0
 #pragma unroll
     for (int i = 0; i < C; i++) {
         const int u = tid + i * nt;
@@ -145,9 +160,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void k_rmsnorm_quant(NormArg
 #pragma unroll
         for (int z = 0; z < 8; z++) v[z] = h[i][z] * w[z];
         if (a.y)
-            *reinterpret_cast<uint4*>(a.y + at + 8 * u) =
-                make_uint4(cvt_bf16x2(v[0] * r, v[1] * r), cvt_bf16x2(v[2] * r, v[3] * r),
-                           cvt_bf16x2(v[4] * r, v[5] * r), cvt_bf16x2(v[6] * r, v[7] * r));
+            store16_nt(a.y + at + 8 * u, bf16x8_of(v, r));
         if constexpr (FP8) {                   // 16 lanes hold a block of 128 channels
             top = 0.0f;
 #pragma unroll
@@ -155,18 +168,23 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void k_rmsnorm_quant(NormArg
             top = group8_max(top);
             top = fmaxf(top, dpp_f32<kDppRowMirror>(top));
         }
-        const float s = top * r / kTop;
+        const float V = top * r;
         if (FP8 ? (u & 15) == 0 : u == 0)
-            a.scales[FP8 ? t * (a.H / 128) + u / 16 : t] = s;
-        // small values first brought to where the factor and its rest are normal
+            a.scales[FP8 ? t * (a.H / 128) + u / 16 : t] = V / kTop;
+        // a scale that rounds to 0 (or is NaN) has no codes. Small values are first
+        // brought to where the factor and its rest are normal; a value is multiplied
+        // by the factor's two parts (f from the reciprocal of the unit, the rest from
+        // what it leaves), so the product is off by its own rounding only
+        const bool live = V > kLeast;
         const float up = top < 0x1p-90f ? 0x1p100f : 1.0f;
-        const float big = top * up;
-        const float f = kTop / big, rest = fmaf(-f, big, kTop) / big;
+        const float big = top * up, inv = __builtin_amdgcn_rcpf(big);
+        const float f = live ? kTop * inv : 0.0f;
+        const float rest = live ? fmaf(-f, big, kTop) * inv : 0.0f;
         float q[8];
 #pragma unroll
         for (int z = 0; z < 8; z++) {
-            const float m = v[z] * up;
-            q[z] = finite && s > 0.0f ? fmaf(m, f, m * rest) : 0.0f;
+            const float n = live ? v[z] * up : 0.0f;
+            q[z] = fmaf(n, f, n * rest);
         }
         uint32_t code[2];
 #pragma unroll
@@ -178,7 +196,8 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void k_rmsnorm_quant(NormArg
                 code[z] = f32x4_to_int8(q[4 * z], q[4 * z + 1], q[4 * z + 2], q[4 * z + 3]);
             }
         }
-        *reinterpret_cast<uint2*>(a.out + at + 8 * u) = make_uint2(code[0], code[1]);
+        __builtin_nontemporal_store(u32x2{code[0], code[1]},
+                                    reinterpret_cast<u32x2*>(a.out + at + 8 * u));
     }
 }
 
@@ -187,7 +206,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void k_rmsnorm_quant(NormArg
 hipError_t launch_rmsnorm_quant(const NormArgs& a, hipStream_t stream, LaunchInfo* info, bool run) {
     const int U = a.H / 8;
     const bool wave_row = U <= 2 * kWave;
-    const int C = wave_row ? (U <= kWave ? 1 : 2) : U <= 1024 ? 1 : U <= 2048 ? 2 : U <= 4096 ? 4 : 8;
+    const int C = wave_row ? (U <= kWave ? 1 : 2) : U <= 2048 ? 2 : U <= 4096 ? 4 : 8;
     const int threads = wave_row ? 256 : (U + C * kWave - 1) / (C * kWave) * kWave;
     const int64_t blocks = wave_row ? (a.T + 3) / 4 : a.T;
     if (info) *info = LaunchInfo{blocks, threads, 0, C, "rmsnorm_quant"};
@@ -202,7 +221,6 @@ hipError_t launch_rmsnorm_quant(const NormArgs& a, hipStream_t stream, LaunchInf
             else launch(k_rmsnorm_quant<F, 2, true>);
         } else {
             switch (C) {
-                case 1: launch(k_rmsnorm_quant<F, 1, false>); break;
                 case 2: launch(k_rmsnorm_quant<F, 2, false>); break;
                 case 4: launch(k_rmsnorm_quant<F, 4, false>); break;
                 default: launch(k_rmsnorm_quant<F, 8, false>);
