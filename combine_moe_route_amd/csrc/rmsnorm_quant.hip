@@ -171,21 +171,23 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void k_rmsnorm_quant(NormArg
         const float V = top * r;
         if (FP8 ? (u & 15) == 0 : u == 0)
             a.scales[FP8 ? t * (a.H / 128) + u / 16 : t] = V / kTop;
-        // a scale that rounds to 0 (or is NaN) has no codes. Small values are first
-        // brought to where the factor and its rest are normal; a value is multiplied
-        // by the factor's two parts (f from the reciprocal of the unit, the rest from
-        // what it leaves), so the product is off by its own rounding only
-        const bool live = V > kLeast;
-        const float up = top < 0x1p-90f ? 0x1p100f : 1.0f;
-        const float big = top * up, inv = __builtin_amdgcn_rcpf(big);
-        const float f = live ? kTop * inv : 0.0f;
-        const float rest = live ? fmaf(-f, big, kTop) * inv : 0.0f;
+        // a value is multiplied by the factor's two parts (f from the reciprocal of the
+        // unit, the rest from what it leaves), so the product is off by its own
+        // rounding only
+        float big = top;
+        if (!(V > kLeast && top >= 0x1p-90f)) {
+            // a scale that rounds to 0, or is NaN, has no codes; small values are first
+            // brought to where the factor and its rest are normal
+            const bool live = V > kLeast;
+            big = live ? top * 0x1p100f : 1.0f;
+#pragma unroll
+            for (int z = 0; z < 8; z++) v[z] = live ? v[z] * 0x1p100f : 0.0f;
+        }
+        const float inv = __builtin_amdgcn_rcpf(big);
+        const float f = kTop * inv, rest = fmaf(-f, big, kTop) * inv;
         float q[8];
 #pragma unroll
-        for (int z = 0; z < 8; z++) {
-            const float n = live ? v[z] * up : 0.0f;
-            q[z] = fmaf(n, f, n * rest);
-        }
+        for (int z = 0; z < 8; z++) q[z] = fmaf(v[z], f, v[z] * rest);
         uint32_t code[2];
 #pragma unroll
         for (int z = 0; z < 2; z++) {

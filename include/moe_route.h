@@ -550,8 +550,8 @@ int moe_grouped_gemm_int8(const void* a, const float* a_scales, const int32_t* e
  *   expert_offsets  device int32 [E+1]; only [E] is read
  *   out             device int8 [max_rows, I] out, 16-byte aligned
  *   out_scales      device fp32 [max_rows] out
- *   I % 16 == 0, 16 <= I <= 32768; 0 <= max_rows < 2^31; 1 <= E <= 1024; rows
- *   above I = 8192 take a workgroup of 1024 threads each (max_rows * 1024 < 2^32)
+ *   I % 16 == 0, 16 <= I <= 32768; 0 <= max_rows < 2^31; 1 <= E <= 1024; the
+ *   launch has to fit a packet (max_rows * 1024 < 2^32 always does)
  * out and out_scales are the a and a_scales of the next moe_grouped_gemm_int8.
  * Rows at or past expert_offsets[E] are neither read nor written; pad rows of a
  * segment (zeros) give zero codes and scales. out and out_scales overlap neither
