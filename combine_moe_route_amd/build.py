@@ -11,10 +11,9 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoeroute.so")
-SOURCES = ["api.hip", "route_topk.hip", "route_scored.hip", "dispatch.hip", "combine.hip",
-           "combine_sender.hip", "grouped_gemm.hip", "grouped_gemm_bf16.hip",
-           "grouped_gemm_int8.hip", "gated_act.hip",
-           "rmsnorm_quant.hip"]
+SOURCES = ["api.hip", "route_topk.hip", "route_scored.hip", "dispatch.hip", "dispatch_direct.hip",
+           "combine.hip", "combine_sender.hip", "grouped_gemm.hip", "grouped_gemm_bf16.hip",
+           "grouped_gemm_int8.hip", "gated_act.hip", "rmsnorm_quant.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

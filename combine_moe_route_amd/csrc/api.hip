@@ -198,7 +198,14 @@ int dispatch_impl(const float* logits, float* topk_w, const void* x, const int32
     moe::LaunchInfo info[4];
     int nk = 0;
     // geometry (route_sort_applies looks only at the logits address)
-    (void)moe::launch_dispatch(a, nullptr, info, &nk, false);
+    auto launch = [&](hipStream_t on, bool go) {
+        if (scales > 0 && moe::dispatch_direct_applies(T, k)) {
+            nk = 1;
+            return moe::launch_dispatch_direct(a, on, info, go);
+        }
+        return moe::launch_dispatch(a, on, info, &nk, go);
+    };
+    (void)launch(nullptr, false);
     if (!all_fit(info, nk)) return MOE_EINVAL;
     // required pointers
     if (!expert_counts || !expert_offsets) return MOE_ENULL;
@@ -233,7 +240,7 @@ int dispatch_impl(const float* logits, float* topk_w, const void* x, const int32
     }
     if (!run) return MOE_OK;
 
-    const hipError_t e = moe::launch_dispatch(a, stream, info, &nk);
+    const hipError_t e = launch(stream, true);
     if (log_enabled())
         for (int i = 0; i < nk; i++) log_launch(info[i].name ? info[i].name : "dispatch", info[i]);
     return status_of(e);

@@ -1,0 +1,200 @@
+// Dispatch of rows that are already quantised, small batches: counting, the scan
+// into offsets and the copy of codes and scales in one launch.
+//
+// Every workgroup reads the whole routing table (at most kDirectPairs slots) and
+// counts it in LDS: one 32-bit counter an expert, the slots of all tokens in its
+// lower half and those of the tokens before the workgroup's own in its upper half,
+// by one atomic a slot. The lower halves, padded and scanned over the experts, are
+// the segment offsets; offset plus upper half is the row of the workgroup's first
+// pair of that expert, and its tokens take theirs one after the other, so the order
+// is the tokens'. The codes are on their way meanwhile. The table is small and comes
+// from L2: no workgroup waits for another, and nothing is kept in a workspace.
+//
+// Against the counting, scanning and copying kernels, us: 1 token of 7168 bytes to 8
+// of 256 experts 8.3 -> 4.6, 128 tokens 9.9 -> 5.6 (one launch instead of two); 2777
+// tokens of 1408 bytes to 6 of 60, 16-row segments 19.6 -> 14.6, 4096 tokens of 1024
+// to 8 of 256 21.2 -> 18.0 (instead of three). What is left is counting (every
+// workgroup, about 5 us at 16 thousand slots) next to the copy. From 32768 slots on
+// the counters' halves could overflow, and counting once is quicker.
+#include "launch.h"
+#include "moe_device.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kBlocks = 1024;              // four to a CU
+constexpr int kWaves = kThreads / kWave;
+constexpr int kRowSlots = 2048;            // slots of a workgroup's tokens: experts, then rows
+constexpr int kPerThread = kMaxExperts / kThreads;
+
+constexpr int kBatch = 4;                  // 16-byte loads of the table in flight
+
+// Four slots of the table, which is aligned to one.
+struct __attribute__((packed, aligned(4))) Quad {
+    int e[4];
+};
+
+struct DirectPlan {
+    int tokens;                            // of a workgroup
+    int blocks, pad_parts, pad_per_expert, pad_rows;   // pad rows of an expert go in parts
+};
+
+__global__ __launch_bounds__(kThreads) void k_dispatch_direct(DispatchArgs a, DirectPlan plan) {
+    __shared__ uint32_t s_run[kMaxExperts];        // counters, then the next row of each expert
+    __shared__ int s_cnt[kMaxExperts], s_off[kMaxExperts + 1], s_row[kRowSlots], s_wave[kWaves];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int E = a.E, k = a.k, T = (int)a.T;
+    const int row_bytes = 2 * a.H, U = row_bytes / 16, CW = (U + kWave - 1) / kWave;
+    const int t0 = min(T, (int)blockIdx.x * plan.tokens), nt = min(plan.tokens, T - t0);
+    const uint8_t* const x = static_cast<const uint8_t*>(a.x);
+    uint8_t* const out = static_cast<uint8_t*>(a.out);
+    // item i of the workgroup: piece i % CW (64 lanes of 16 bytes) of token t0 + i / CW
+    auto load = [&](int i) {
+        const int64_t t = t0 + i / CW;
+        return load16_nt(range_rsrc(x + t * row_bytes, row_bytes), 16 * ((i % CW) * kWave + lane));
+    };
+    uint4 piece = make_uint4(0u, 0u, 0u, 0u);
+    if (wave < nt * CW) piece = load(wave);
+
+    for (int e = tid; e < E; e += kThreads) s_run[e] = 0;
+    for (int p = tid; p < nt * k; p += kThreads) s_row[p] = a.topk_idx[t0 * k + p];
+    __syncthreads();
+    const int pairs = T * k, own = t0 * k, quads = pairs / 4;
+    auto count = [&](int p, int e) {
+        if ((unsigned)e < (unsigned)E) atomicAdd(&s_run[e], p < own ? 0x10001u : 1u);
+    };
+    for (int q0 = tid; q0 < quads; q0 += kBatch * kThreads) {
+        Quad v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; i++) {
+            const int q = q0 + i * kThreads;
+            v[i] = Quad{{-1, -1, -1, -1}};
+            if (q < quads) v[i] = reinterpret_cast<const Quad*>(a.topk_idx)[q];
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; i++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) count(4 * (q0 + i * kThreads) + c, v[i].e[c]);
+    }
+    if (tid < pairs - 4 * quads) count(4 * quads + tid, a.topk_idx[4 * quads + tid]);
+    __syncthreads();
+    int cnt[kPerThread], padded[kPerThread], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPerThread; i++) {
+        const int e = kPerThread * tid + i;
+        cnt[i] = e < E ? (int)(s_run[e] & 0xFFFFu) : 0;
+        padded[i] = (cnt[i] + a.row_align - 1) / a.row_align * a.row_align;
+        sum += padded[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int v = __shfl_up(incl, d, kWave);
+        if (lane >= d) incl += v;
+    }
+    if (lane == kWave - 1) s_wave[wave] = incl;
+    __syncthreads();
+    int at = incl - sum;
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) at += w < wave ? s_wave[w] : 0;
+#pragma unroll
+    for (int i = 0; i < kPerThread; i++) {
+        const int e = kPerThread * tid + i;
+        if (e < E) {
+            s_off[e] = at;
+            s_cnt[e] = cnt[i];
+            s_run[e] = at + (s_run[e] >> 16);
+            if (blockIdx.x == 0) {
+                a.expert_counts[e] = cnt[i];
+                a.expert_offsets[e] = at;
+            }
+            if (e == E - 1) {
+                s_off[E] = at + padded[i];
+                if (blockIdx.x == 0) a.expert_offsets[E] = at + padded[i];
+            }
+        }
+        at += padded[i];
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && a.group_offsets != nullptr)
+        for (int g = tid; g <= a.groups; g += kThreads)
+            a.group_offsets[g] = s_off[g * (E / a.groups)];
+
+    for (int i = 0; i < nt; i++) {
+        for (int j = tid; j < k; j += kThreads) {
+            const int p = (t0 + i) * k + j, e = s_row[i * k + j];
+            int r = -1;
+            if ((unsigned)e < (unsigned)E) {
+                r = (int)atomicAdd(&s_run[e], 1u);
+                if (r < 0 || r >= a.max_rows) r = -1;        // never write outside
+            }
+            s_row[i * k + j] = r;
+            a.dst_row[p] = r;
+            if (r >= 0) {
+                a.row_src[r] = p;
+                if (a.scales == 1) a.out_scales[r] = a.x_scales[t0 + i];
+            }
+        }
+        __syncthreads();                   // the next token's rows follow this one's
+    }
+    for (int i = wave; i < nt * CW; i += kWaves) {
+        const int t = i / CW, u = (i % CW) * kWave + lane;
+        if (i != wave) piece = load(i);
+        for (int j = 0; j < k; j++) {
+            const int r = __builtin_amdgcn_readfirstlane(s_row[t * k + j]);
+            if (r >= 0 && u < U)
+                store16_nt(out + (int64_t)r * row_bytes + 16 * (int64_t)u, piece);
+        }
+        if (a.scales > 1 && i % CW == 0) {
+            for (int c = lane; c < a.scales; c += kWave) {
+                const float s = a.x_scales[(int64_t)(t0 + t) * a.scales + c];
+                for (int j = 0; j < k; j++) {
+                    const int r = s_row[t * k + j];
+                    if (r >= 0) a.out_scales[(int64_t)r * a.scales + c] = s;
+                }
+            }
+        }
+    }
+    for (int pb = blockIdx.x; pb < plan.pad_parts; pb += plan.blocks) {
+        const int e = pb / plan.pad_per_expert, part = pb % plan.pad_per_expert;
+        const int first = s_off[e] + s_cnt[e] + part * plan.pad_rows;
+        const int rows = min(s_off[e + 1] - first, plan.pad_rows);
+        for (int i = tid; i < rows * U; i += kThreads)
+            *reinterpret_cast<uint4*>(out + (int64_t)first * row_bytes + 16 * (int64_t)i) =
+                make_uint4(0u, 0u, 0u, 0u);
+        for (int i = tid; i < rows * a.scales; i += kThreads)
+            a.out_scales[(int64_t)first * a.scales + i] = 0.0f;
+        for (int i = tid; i < rows; i += kThreads) a.row_src[first + i] = -1;
+    }
+}
+
+}  // namespace
+
+bool dispatch_direct_applies(int64_t T, int k) { return T * k <= kDirectPairs; }
+
+hipError_t launch_dispatch_direct(const DispatchArgs& a, hipStream_t stream, LaunchInfo* info,
+                                  bool run) {
+    DirectPlan plan;
+    // one workgroup a token while all of them run at once (four a CU), then more tokens
+    // each, since every workgroup counts the whole table: 2777 tokens x 6 of 60 experts,
+    // 1408 bytes, us: 1024 workgroups 15.4, 512 16.1, 2048 19.1
+    int64_t tokens = (a.T + kBlocks - 1) / kBlocks;
+    if (tokens * a.k > kRowSlots) tokens = kRowSlots / a.k;
+    plan.tokens = tokens < 1 ? 1 : (int)tokens;
+    plan.pad_per_expert = a.T > 0 && a.row_align > 1 ? (a.row_align - 1 < 4 ? a.row_align - 1 : 4) : 0;
+    plan.pad_parts = a.E * plan.pad_per_expert;
+    plan.pad_rows = plan.pad_parts ? (a.row_align + plan.pad_per_expert - 2) / plan.pad_per_expert : 0;
+    const int64_t token_blocks = (a.T + plan.tokens - 1) / plan.tokens;
+    const int64_t least = plan.pad_parts < kBlocks ? plan.pad_parts : kBlocks;
+    plan.blocks = (int)(token_blocks > least ? token_blocks : least);
+    if (plan.blocks < 1) plan.blocks = 1;              // no tokens: the tables
+    if (info) *info = LaunchInfo{plan.blocks, kThreads, 0, plan.tokens, "count+scan+scatter"};
+    if (!run) return hipSuccess;
+    k_dispatch_direct<<<dim3((unsigned)plan.blocks), dim3(kThreads), 0, stream>>>(a, plan);
+    return hipGetLastError();
+}
+
+}  // namespace moe

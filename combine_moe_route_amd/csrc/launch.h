@@ -83,6 +83,13 @@ DispatchWorkspace dispatch_workspace(int64_t T, int E, int k);
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t stream, LaunchInfo info[4], int* n,
                            bool run = true);
 
+// Rows already quantised (scales > 0), at most kDirectPairs slots: one kernel that
+// needs no workspace.
+constexpr int64_t kDirectPairs = 32768;
+bool dispatch_direct_applies(int64_t T, int k);
+hipError_t launch_dispatch_direct(const DispatchArgs& a, hipStream_t stream, LaunchInfo* info,
+                                  bool run = true);
+
 hipError_t launch_combine(const void* expert_out, const int32_t* dst_row, const float* topk_w,
                           int64_t T, int H, int k, void* y, hipStream_t stream,
                           LaunchInfo* info, bool run = true);

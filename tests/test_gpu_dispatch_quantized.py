@@ -69,6 +69,40 @@ def test_layout(T, H, S, E, k, groups, align):
     check(T, H, S, E, k, groups, align)
 
 
+@pytest.mark.parametrize("T,H,S,E,k,groups,align", [
+    (32, 16, 0, 1024, 1024, 1, 1), (33, 16, 1, 1000, 1000, 4, 2), (32768, 16, 0, 1, 1, 1, 1),
+    (32769, 16, 0, 1, 1, 1, 1), (16384, 32, 2, 3, 2, 3, 8), (16385, 32, 2, 3, 2, 3, 8),
+    (4096, 48, 0, 8, 8, 1, 5), (1500, 1040, 3, 2, 2, 1, 100), (1024, 64, 0, 64, 64, 1, 1),
+    (7, 16, 0, 1024, 3, 1, 1024),
+])
+def test_around_the_limit_of_one_launch(T, H, S, E, k, groups, align):
+    """32768 slots and a few more; many slots a token; experts that every token
+    chooses."""
+    check(T, H, S, E, k, groups, align)
+
+
+@pytest.mark.parametrize("T", [90, 5000])
+def test_one_hot_expert_and_unaligned_table(T):
+    """Every token's first choice is the same expert; the table starts at an odd
+    element, and ids out of range of either sign are dropped."""
+    from combine_moe_route_amd import moe_dispatch_quantized
+    log(f"dispatch_quantized hot T={T}")
+    idx = routing(T, 30, 3, 5) + 1
+    idx[:, 0] = 0
+    idx[5, 1], idx[6, 2], idx[7, 0] = 31, -2 ** 31, 2 ** 31 - 1
+    flat = torch.zeros(3 * T + 1, dtype=torch.int32, device=DEV)
+    flat[1:] = torch.from_numpy(idx.reshape(-1)).to(DEV)
+    codes = np.random.default_rng(1).integers(0, 256, (T, 32), dtype=np.uint8)
+    b = moe_dispatch_quantized(torch.from_numpy(codes).to(DEV), torch.ones(T, device=DEV),
+                               flat[1:].view(T, 3), 31, 1, 4)
+    ref = oracle.dispatch(codes.view(np.uint16), idx, 31, 1, 4, False)
+    R = ref.num_rows
+    assert np.array_equal(b.dst_row.cpu().numpy(), ref.dst_row)
+    assert np.array_equal(b.row_src[:R].cpu().numpy(), ref.row_src)
+    assert np.array_equal(b.out[:R].cpu().numpy().view(np.uint16), ref.out)
+    assert np.array_equal(b.expert_counts.cpu().numpy(), ref.expert_counts)
+
+
 def test_dropped_slots_and_bytes():
     check(500, 96, 3, 12, 4, align=8, seed=1, dropped=0.3)
     check(40, 96, 0, 12, 4, align=1, seed=2, dropped=1.0)
