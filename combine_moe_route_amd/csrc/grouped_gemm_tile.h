@@ -667,7 +667,11 @@ template <typename P, typename SH>
 hipError_t launch_shape(const GroupedGemmArgs& g, hipStream_t stream, LaunchInfo* info, bool run) {
     const int n_out = g.gated ? g.N / 2 : g.N;
     const int out_cols = g.gated ? SH::kBN / 2 : SH::kBN;
-    const int64_t max_tiles = (g.max_rows + SH::kBM - 1) / SH::kBM + g.E;
+    // m segments that have rows hold at most m + (max_rows - m) / kBM tiles. A tile that
+    // no segment has costs a workgroup that finds this out: with max_rows / kBM + E
+    // tiles, 1 token through 2 of 8 experts launched four times what it needed.
+    const int64_t m = g.E < g.max_rows ? g.E : g.max_rows;
+    const int64_t max_tiles = m + (g.max_rows - m) / SH::kBM;
     const int64_t items = max_tiles * ((n_out + out_cols - 1) / out_cols);
     const int64_t grid = (items + kXcds - 1) / kXcds * kXcds;
     constexpr bool kStreamed = std::is_same_v<SH, Skinny<true>>;
