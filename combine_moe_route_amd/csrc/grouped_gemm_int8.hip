@@ -12,13 +12,44 @@
 
 namespace moe {
 
+// The shape of a call, from what the host knows: the capacity, from which the
+// rows of an expert that has any, r (with padded segments more than there are).
+//
+// r <= 20: Skinny, whose tile holds a segment of average length. Segments longer than
+// its 32 rows read their weights again: 256 experts, K 7168, N 4096, ragged segments
+// of mean r, us:
+//   r                   4     8    16    24    32    48
+//   Skinny           1060  1110  1183  1358  1924  2679
+//   Medium           1187  1218  1241  1259  1277  1306
+// With rows of whole 128-byte lines (K % 128 == 0) the weights are streamed with the
+// non-temporal hint (7.3 TB/s at r = 4; without it 1167 us). Lines that two k-blocks
+// share would be fetched twice.
+//
+// Otherwise the shape of least estimated time: rounds of the chip times the time of a
+// round, start + k-blocks times a rate that grows with the share of the chip that is
+// busy (us). Measured, experts x rows, K, N (* the choice):
+//                          Large  Medium  Small  Skinny
+//   16 x 400, 4096, 4096    132*    143    157     423
+//    8 x 1000, 8192, 4096   235*    281    308     894
+//   16 x 1024, 7168, 4096   425*    528    574    1571
+//    1 x 2048, 8192, 4096    77      66*    68     196
+//   55 x 286, 784, 2336     119      99     94*    242
+//   37 x 480, 288, 2352      62      54     54*    199
+//   12 x 194, 2032, 1032     30      20     17*     29
+//   20 x 450, 3600, 904      48*     57     61     117
+//    1 x 128, 8192, 4096     72      40     34      19*
+//    5 x 217, 9168, 416      82      61     45      23*
+// A segment ends inside a tile, half a tile on average; a lone segment's tiles are
+// known. The last round counts a quarter more than its share. Skinny is for launches
+// that it fits on the chip in one round: with more, its estimate misses that weights
+// are read again.
 hipError_t launch_grouped_gemm_int8(const GroupedGemmArgs& g, hipStream_t stream, LaunchInfo* info,
                                     bool run) {
     const int64_t hit = g.E < g.max_rows ? g.E : g.max_rows;
     const double r = hit ? (double)g.max_rows / hit : 0.0;
-    if (r <= 32.0)
-        return g.K % 64 == 0 ? launch_shape<Int8, Skinny<true>>(g, stream, info, run)
-                             : launch_shape<Int8, Skinny<false>>(g, stream, info, run);
+    if (r <= 20.0)
+        return g.K % kBK == 0 ? launch_shape<Int8, Skinny<true>>(g, stream, info, run)
+                              : launch_shape<Int8, Skinny<false>>(g, stream, info, run);
     const double kb = (g.K + kBK - 1) / kBK;
     auto items = [&](int bm, int bn) {
         double per = r / bm + 0.5;
@@ -26,11 +57,15 @@ hipError_t launch_grouped_gemm_int8(const GroupedGemmArgs& g, hipStream_t stream
         return hit * (per > 1.0 ? per : 1.0) * ((g.N + bn - 1) / bn);
     };
     auto rounds = [](double n, int slots) { return n <= slots ? 1.0 : n / slots + 0.25; };
-    const double small_n = items(128, 128), skinny_n = items(32, 64);
-    const double large = rounds(items(256, 256), 256) * (12.0 + 1.6 * kb);
-    const double medium = rounds(items(128, 256), 256) * (8.0 + 1.0 * kb);
+    auto busy = [](double n) { return n < 256 ? n / 256 : 1.0; };
+    const double large_n = items(256, 256), medium_n = items(128, 256), small_n = items(128, 128);
+    const double skinny_n = items(32, 64);
+    const double large = rounds(large_n, 256) * (12.0 + (1.0 + 0.6 * busy(large_n)) * kb);
+    const double medium = rounds(medium_n, 256) * (8.0 + (0.65 + 0.35 * busy(medium_n)) * kb);
     const double small = small_n <= 256 ? 5.0 + 0.55 * kb : rounds(small_n, 512) * (6.0 + 1.1 * kb);
-    const double skinny = skinny_n <= 256 ? 2.0 + 0.23 * kb : rounds(skinny_n, 512) * (3.0 + 0.4 * kb);
+    const double skinny = skinny_n <= 256   ? 2.0 + 0.23 * kb
+                          : skinny_n <= 512 ? 3.0 + 0.4 * kb
+                                            : 1e30;
     if (large <= medium && large <= small && large <= skinny)
         return launch_shape<Int8, Large>(g, stream, info, run);
     if (medium <= small && medium <= skinny) return launch_shape<Int8, Medium>(g, stream, info, run);
