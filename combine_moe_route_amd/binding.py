@@ -159,8 +159,9 @@ def _addr(t: Optional[torch.Tensor]):
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape=None, device=None):
-    if (t.dtype is dtype and t.is_cuda and (device is None or t.device == device)
-            and t.is_contiguous() and (shape is None or t.shape == shape)):
+    # (a CPU device has no index, so it never passes here)
+    if (t.dtype is dtype and (t.is_cuda if device is None else t.get_device() == device.index)
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
         return
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -466,7 +467,7 @@ def moe_dispatch_quantized(x: torch.Tensor, x_scales: torch.Tensor, topk_idx: to
     if bufs is None:
         bufs = alloc_dispatch_quantized(T, H, E, k, groups, row_align, x.dtype,
                                         tail[0] if tail else None, dev)
-    R = moe_dispatch_max_rows(T, E, k, row_align)
+    R = T * k + E * (row_align - 1)     # moe_dispatch_max_rows; the library checks the limits
     _need(bufs.out, "out", x.dtype, (R, H), dev)
     _need(bufs.out_scales, "out_scales", torch.float32, (R,) + tail, dev)
     _need(bufs.expert_counts, "expert_counts", torch.int32, (E,), dev)

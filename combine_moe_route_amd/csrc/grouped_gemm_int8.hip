@@ -12,6 +12,20 @@
 
 namespace moe {
 
+// Skinny tiles of 64 weight rows, or of 32 where those would leave half of the chip
+// idle: a CU takes in no more than about 35 GB/s here, whatever is in flight (twice
+// the waves a workgroup changed nothing). 16 rows, K 7168, N 2400: 17.5 -> 12.9 us;
+// one row, K 2048, N 7168: 8.1 -> 6.7; K 130000, N 64: 148 -> 98; but with 256 tiles
+// of 64, 128 rows, K 8192, N 4096: 18.6 -> 24.5.
+static hipError_t launch_skinny(const GroupedGemmArgs& g, double tiles, bool streamed,
+                                hipStream_t stream, LaunchInfo* info, bool run) {
+    if (tiles <= 128.0 && !g.gated)
+        return streamed ? launch_shape<Int8, Skinny<true, 32>>(g, stream, info, run)
+                        : launch_shape<Int8, Skinny<false, 32>>(g, stream, info, run);
+    return streamed ? launch_shape<Int8, Skinny<true>>(g, stream, info, run)
+                    : launch_shape<Int8, Skinny<false>>(g, stream, info, run);
+}
+
 // The shape of a call, from what the host knows: the capacity, from which the
 // rows of an expert that has any, r (with padded segments more than there are).
 //
@@ -47,9 +61,6 @@ hipError_t launch_grouped_gemm_int8(const GroupedGemmArgs& g, hipStream_t stream
                                     bool run) {
     const int64_t hit = g.E < g.max_rows ? g.E : g.max_rows;
     const double r = hit ? (double)g.max_rows / hit : 0.0;
-    if (r <= 20.0)
-        return g.K % kBK == 0 ? launch_shape<Int8, Skinny<true>>(g, stream, info, run)
-                              : launch_shape<Int8, Skinny<false>>(g, stream, info, run);
     const double kb = (g.K + kBK - 1) / kBK;
     auto items = [&](int bm, int bn) {
         double per = r / bm + 0.5;
@@ -58,8 +69,9 @@ hipError_t launch_grouped_gemm_int8(const GroupedGemmArgs& g, hipStream_t stream
     };
     auto rounds = [](double n, int slots) { return n <= slots ? 1.0 : n / slots + 0.25; };
     auto busy = [](double n) { return n < 256 ? n / 256 : 1.0; };
-    const double large_n = items(256, 256), medium_n = items(128, 256), small_n = items(128, 128);
     const double skinny_n = items(32, 64);
+    if (r <= 20.0) return launch_skinny(g, skinny_n, g.K % kBK == 0, stream, info, run);
+    const double large_n = items(256, 256), medium_n = items(128, 256), small_n = items(128, 128);
     const double large = rounds(large_n, 256) * (12.0 + (1.0 + 0.6 * busy(large_n)) * kb);
     const double medium = rounds(medium_n, 256) * (8.0 + (0.65 + 0.35 * busy(medium_n)) * kb);
     const double small = small_n <= 256 ? 5.0 + 0.55 * kb : rounds(small_n, 512) * (6.0 + 1.1 * kb);
@@ -70,7 +82,7 @@ hipError_t launch_grouped_gemm_int8(const GroupedGemmArgs& g, hipStream_t stream
         return launch_shape<Int8, Large>(g, stream, info, run);
     if (medium <= small && medium <= skinny) return launch_shape<Int8, Medium>(g, stream, info, run);
     if (small <= skinny) return launch_shape<Int8, Small>(g, stream, info, run);
-    return launch_shape<Int8, Skinny<false>>(g, stream, info, run);
+    return launch_skinny(g, skinny_n, false, stream, info, run);
 }
 
 }  // namespace moe

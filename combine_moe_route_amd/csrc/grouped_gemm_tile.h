@@ -440,8 +440,8 @@ __device__ __forceinline__ void tile_body(const GroupedGemmArgs& g, const Tile& 
 //   Large   256 x 256, 4 waves of 128 x 128, 2 + 3, one workgroup per CU
 //   Medium  128 x 256, 8 waves of 64 x 64, 3 + 3, one per CU
 //   Small   128 x 128, 4 waves of 64 x 64, 2 + 3, two per CU
-//   Skinny  32 x 64, see below, two per CU; STREAM loads the weights with the
-//           non-temporal hint
+//   Skinny  32 x 64 (or x 32), see below, two per CU or more; STREAM loads the
+//           weights with the non-temporal hint
 struct Large {
     static constexpr int kBM = 256, kBN = 256, kThreads = 256, kLds = 163840;
 };
@@ -451,9 +451,10 @@ struct Medium {
 struct Small {
     static constexpr int kBM = 128, kBN = 128, kThreads = 256, kLds = 81920;
 };
-template <bool STREAM>
+template <bool STREAM, int BN = 64>
 struct Skinny {
-    static constexpr int kBM = 32, kBN = 64, kThreads = 256, kLds = 65536;
+    static constexpr int kBM = 32, kBN = BN, kThreads = 256, kLds = 1024 * BN;
+    static constexpr bool kStream = STREAM;
 };
 
 template <typename P, typename SH, bool GATED>
@@ -532,23 +533,25 @@ __device__ __forceinline__ void skinny_store(const GroupedGemmArgs& g, const Til
     }
 }
 
-// One tile of 32 rows and 64 weight rows; the inner dimension is split over
+// One tile of 32 rows and 64 (or 32) weight rows; the inner dimension is split over
 // the 4 waves (wave w takes k-blocks w, w + 4, ...), which read nothing of each
 // other until their sums are joined at the end. A wave streams its weight
 // k-blocks through two LDS stages of its own and holds the activations of the
 // same k-blocks in registers (a fragment is 16 bytes a lane, straight from the
 // row), so it meets no barrier and two workgroups fit a CU.
-template <typename P, bool STREAM, bool GATED>
-__global__ __launch_bounds__(Skinny<STREAM>::kThreads, 2) void k_grouped_gemm_skinny(
-    GroupedGemmArgs g) {
-    constexpr int kWaves = 4, kStage = 64 * kBK * 2;     // 8 KB of weights
+template <typename P, typename SH, bool GATED>
+__global__ __launch_bounds__(SH::kThreads, 2) void k_grouped_gemm_skinny(GroupedGemmArgs g) {
+    constexpr bool STREAM = SH::kStream;
+    constexpr int kWaves = 4, JF = SH::kBN / 32;         // groups of 32 weight rows
+    static_assert(JF == 2 || (JF == 1 && !GATED), "gate and up rows are a group each");
+    constexpr int kStage = SH::kBN * kBK * 2;            // 8 KB of weights, or 4
     __shared__ __attribute__((aligned(1024))) uint8_t s0[kWaves * kStage], s1[kWaves * kStage];
     const int K = g.K, KB = (K + kBK - 1) / kBK;
     const int n_out = GATED ? g.N / 2 : g.N;
-    constexpr int kOutCols = GATED ? 32 : 64;
+    constexpr int kOutCols = GATED ? 32 : SH::kBN;
     Tile td;
     int nt;
-    if (!find_tile<32, Skinny<STREAM>::kThreads>(g.off, g.E, (int)g.max_rows,
+    if (!find_tile<32, SH::kThreads>(g.off, g.E, (int)g.max_rows,
                                          (n_out + kOutCols - 1) / kOutCols,
                                          reinterpret_cast<int*>(s0), td, nt))
         return;
@@ -571,7 +574,7 @@ __global__ __launch_bounds__(Skinny<STREAM>::kThreads, 2) void k_grouped_gemm_sk
     }
     const int a_row = (lane & 31) * K * 2;
     u32x4 af[2][4];
-    // this wave's k-blocks: wave + 4 ((i + turn) mod n). Every tile starts at
+    // this wave's k-blocks: wave + kWaves ((i + turn) mod n). Every tile starts at
     // another place, so that workgroups that run in step do not all read the
     // same columns of rows a power of two apart, which are the same memory
     // channels (one token through 2 of 8 experts, K 4096, N 16384: 46 us, without
@@ -592,7 +595,7 @@ __global__ __launch_bounds__(Skinny<STREAM>::kThreads, 2) void k_grouped_gemm_sk
                 ra, c < K ? a_row + c * 2 : kOutOfRange, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 8; i++)
+        for (int i = 0; i < 4 * JF; i++)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rw[i / 4], (__attribute__((address_space(3))) void*)(s + i * 1024), 16,
                 k0 + kc[i & 1] < K ? w_off[i & 1] + i % 4 * 8 * K + k0 * 2 : kOutOfRange, 0, 0,
@@ -601,28 +604,28 @@ __global__ __launch_bounds__(Skinny<STREAM>::kThreads, 2) void k_grouped_gemm_sk
     };
     using Frag = typename P::Frag;
     using Acc4 = typename P::Acc4;
-    typename P::Acc acc[2];
+    typename P::Acc acc[JF];
 #pragma unroll
-    for (int j = 0; j < 2; j++)
+    for (int j = 0; j < JF; j++)
 #pragma unroll
         for (int x = 0; x < 16; x++) acc[j][x] = 0;
     const int fr = (lane & 31) * 128;
     auto step = [&](auto stage, int i) {
         constexpr int ST = decltype(stage)::value;
-        wait_vmcnt<12>();                                // all but the k-block behind this one
+        wait_vmcnt<4 + 4 * JF>();                        // all but the k-block behind this one
         __builtin_amdgcn_sched_barrier(0);
         const uint8_t* s = (ST ? s1 : s0) + wave * kStage + fr;
-        Frag wf[4][2];
+        Frag wf[4][JF];
 #pragma unroll
         for (int q = 0; q < 4; q++)
 #pragma unroll
-            for (int j = 0; j < 2; j++)
+            for (int j = 0; j < JF; j++)
                 wf[q][j] = *reinterpret_cast<const Frag*>(
                     s + j * 4096 + (((2 * q + (lane >> 5)) ^ chunk_key(lane & 31)) << 4));
 #pragma unroll
         for (int q = 0; q < 4; q++)
 #pragma unroll
-            for (int j = 0; j < 2; j++)
+            for (int j = 0; j < JF; j++)
                 acc[j] = P::mma(wf[q][j], __builtin_bit_cast(Frag, af[ST][q]), acc[j]);
         issue(stage, i + 2);
     };
@@ -639,21 +642,21 @@ __global__ __launch_bounds__(Skinny<STREAM>::kThreads, 2) void k_grouped_gemm_sk
     wait_vmcnt<0>();
     // join: wave w finishes columns 16 h + 4 w .. +3 of every row, from the
     // four waves' sums in order
-    Acc4* const join = reinterpret_cast<Acc4*>(s0);    // [wave][j][x / 4][lane], 32 KB
+    Acc4* const join = reinterpret_cast<Acc4*>(s0);      // [wave][j][x / 4][lane], 16 KB a group
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 2; j++)
+    for (int j = 0; j < JF; j++)
 #pragma unroll
         for (int x = 0; x < 4; x++)
-            join[((wave * 2 + j) * 4 + x) * 64 + lane] =
+            join[((wave * JF + j) * 4 + x) * 64 + lane] =
                 Acc4{acc[j][4 * x], acc[j][4 * x + 1], acc[j][4 * x + 2], acc[j][4 * x + 3]};
     __syncthreads();
-    Acc4 z[2];
+    Acc4 z[2] = {};
 #pragma unroll
-    for (int j = 0; j < 2; j++) {
+    for (int j = 0; j < JF; j++) {
         z[j] = join[(j * 4 + wave) * 64 + lane];
 #pragma unroll
-        for (int w = 1; w < kWaves; w++) z[j] += join[((w * 2 + j) * 4 + wave) * 64 + lane];
+        for (int w = 1; w < kWaves; w++) z[j] += join[((w * JF + j) * 4 + wave) * 64 + lane];
     }
     switch (g.act) {
         case kActRelu: skinny_store<P, kActRelu, GATED>(g, td, o0, cols, z[0], z[1]); break;
@@ -674,15 +677,23 @@ hipError_t launch_shape(const GroupedGemmArgs& g, hipStream_t stream, LaunchInfo
     const int64_t max_tiles = m + (g.max_rows - m) / SH::kBM;
     const int64_t items = max_tiles * ((n_out + out_cols - 1) / out_cols);
     const int64_t grid = (items + kXcds - 1) / kXcds * kXcds;
-    constexpr bool kStreamed = std::is_same_v<SH, Skinny<true>>;
+    constexpr bool kSkinny = SH::kBN <= 64;
+    constexpr bool kStreamed = [] {
+        if constexpr (kSkinny) return SH::kStream;
+        else return false;
+    }();
     if (info)
         *info = LaunchInfo{grid, SH::kThreads, (size_t)SH::kLds, SH::kBM,
                            kStreamed ? P::kStreamedName : P::kName};
     if (!run) return hipSuccess;
     const dim3 blocks((unsigned)grid), threads(SH::kThreads);
-    if constexpr (SH::kBN == 64) {
-        if (g.gated) k_grouped_gemm_skinny<P, kStreamed, true><<<blocks, threads, 0, stream>>>(g);
-        else k_grouped_gemm_skinny<P, kStreamed, false><<<blocks, threads, 0, stream>>>(g);
+    if constexpr (kSkinny) {
+        if constexpr (SH::kBN == 64) {
+            if (g.gated) k_grouped_gemm_skinny<P, SH, true><<<blocks, threads, 0, stream>>>(g);
+            else k_grouped_gemm_skinny<P, SH, false><<<blocks, threads, 0, stream>>>(g);
+        } else {
+            k_grouped_gemm_skinny<P, SH, false><<<blocks, threads, 0, stream>>>(g);
+        }
     } else {
         if (g.gated) k_grouped_gemm<P, SH, true><<<blocks, threads, 0, stream>>>(g);
         else k_grouped_gemm<P, SH, false><<<blocks, threads, 0, stream>>>(g);
