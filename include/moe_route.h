@@ -319,8 +319,8 @@ int moe_dispatch_quantized(const void* x, const float* x_scales, const int32_t* 
  *   out_scales   device fp32 out: [T] (int8) or [T, H/128] (fp8)
  *   H            8 <= H <= 65536, H % 8 == 0 (int8) or H % 128 == 0 (fp8)
  *   eps          1e-30 <= eps <= 1
- *   T >= 0 (T == 0 is a no-op), T * ld_x <= 2^40, ld_x <= 2^31, T * 1024 < 2^32
- *   at most
+ *   T >= 0 (T == 0 is a no-op), T * ld_x <= 2^40, ld_x <= 2^31; the launch has to
+ *   fit a packet (T * 1024 < 2^32 always does)
  * A token with an infinity or NaN in h (also one that the addition made) gets NaN
  * in y and in its scales and zero codes. Outputs overlap neither inputs nor each
  * other, but for sum == residual (MOE_EINVAL; the gaps between rows of x are free).

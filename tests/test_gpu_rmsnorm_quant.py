@@ -157,6 +157,24 @@ def test_values():
     check(x, res, (w.float() * 1e-36).to(torch.bfloat16), "fp8")
 
 
+def test_largest_weights_and_x_as_its_own_residual():
+    log("rmsnorm large weights")
+    x, _, w = make(10, 2048, False, 4, loud=False)
+    x[3:] *= 2.0 ** 58
+    x[6:] *= 2.0 ** 60
+    w = (w.float() * 2.0 ** 58).to(torch.bfloat16)
+    w[7] = 2.0 ** 60
+    for quant in ("int8", "fp8"):
+        check(x, None, w, quant)
+        check(x, x, w, quant)
+
+
+def test_many_short_rows():
+    log("rmsnorm many rows")
+    check(*make(300_001, 8, True, 4), "int8")
+    check(*make(70_003, 128, True, 5), "fp8", in_place=True)
+
+
 def test_non_finite_tokens():
     """A token with an infinity or NaN gets NaN scales and zero codes; the others
     are as without it."""
