@@ -44,5 +44,7 @@ __all__ = list(_API)
 def __getattr__(name):
     if name in _API:
         from . import binding
-        return getattr(binding, name)
+        # found directly from now on: coming here costs 0.5 us a call
+        value = globals()[name] = getattr(binding, name)
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
