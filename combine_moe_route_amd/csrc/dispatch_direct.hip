@@ -6,16 +6,17 @@
 // lower half and those of the tokens before the workgroup's own in its upper half,
 // by one atomic a slot. The lower halves, padded and scanned over the experts, are
 // the segment offsets; offset plus upper half is the row of the workgroup's first
-// pair of that expert, and its tokens take theirs one after the other, so the order
-// is the tokens'. The codes are on their way meanwhile. The table is small and comes
-// from L2: no workgroup waits for another, and nothing is kept in a workspace.
+// slot of that expert, and each of its slots adds the number of those before it, so
+// the order is the tokens'. The codes are on their way meanwhile. The table is small
+// and comes from L2: no workgroup waits for another, and nothing is kept in a
+// workspace.
 //
 // Against the counting, scanning and copying kernels, us: 1 token of 7168 bytes to 8
-// of 256 experts 8.3 -> 4.6, 128 tokens 9.9 -> 5.6 (one launch instead of two); 2777
-// tokens of 1408 bytes to 6 of 60, 16-row segments 19.6 -> 14.6, 4096 tokens of 1024
-// to 8 of 256 21.2 -> 18.0 (instead of three). What is left is counting (every
-// workgroup, about 5 us at 16 thousand slots) next to the copy. From 32768 slots on
-// the counters' halves could overflow, and counting once is quicker.
+// of 256 experts 8.3 -> 4.8, 128 tokens 9.9 -> 5.7 (one launch instead of two); 2777
+// tokens of 1408 bytes to 6 of 60, 16-row segments 19.6 -> 12.2, 4096 tokens of 1024
+// to 8 of 256 21.2 -> 14.9 (instead of three). What is left is counting (in every
+// workgroup, about 4 us at 16 thousand slots) next to the copy. Past 32768 slots the
+// counters' halves could overflow.
 #include "launch.h"
 #include "moe_device.h"
 
@@ -23,12 +24,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kBlocks = 1024;              // four to a CU
-constexpr int kWaves = kThreads / kWave;
-constexpr int kRowSlots = 2048;            // slots of a workgroup's tokens: experts, then rows
-constexpr int kPerThread = kMaxExperts / kThreads;
-
+constexpr int kRowSlots = 2048;            // slots of a workgroup's tokens
 constexpr int kBatch = 4;                  // 16-byte loads of the table in flight
 
 // Four slots of the table, which is aligned to one.
@@ -41,9 +37,12 @@ struct DirectPlan {
     int blocks, pad_parts, pad_per_expert, pad_rows;   // pad rows of an expert go in parts
 };
 
+template <int kThreads>
 __global__ __launch_bounds__(kThreads) void k_dispatch_direct(DispatchArgs a, DirectPlan plan) {
-    __shared__ uint32_t s_run[kMaxExperts];        // counters, then the next row of each expert
+    constexpr int kWaves = kThreads / kWave, kPerThread = kMaxExperts / kThreads;
+    __shared__ uint32_t s_run[kMaxExperts];        // counters, then each expert's first row here
     __shared__ int s_cnt[kMaxExperts], s_off[kMaxExperts + 1], s_row[kRowSlots], s_wave[kWaves];
+    __shared__ __attribute__((aligned(16))) int s_id[kRowSlots];
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int E = a.E, k = a.k, T = (int)a.T;
@@ -56,11 +55,12 @@ __global__ __launch_bounds__(kThreads) void k_dispatch_direct(DispatchArgs a, Di
         const int64_t t = t0 + i / CW;
         return load16_nt(range_rsrc(x + t * row_bytes, row_bytes), 16 * ((i % CW) * kWave + lane));
     };
+    const float first_scale = nt > 0 && a.scales == 1 ? a.x_scales[t0] : 0.0f;
     uint4 piece = make_uint4(0u, 0u, 0u, 0u);
     if (wave < nt * CW) piece = load(wave);
 
     for (int e = tid; e < E; e += kThreads) s_run[e] = 0;
-    for (int p = tid; p < nt * k; p += kThreads) s_row[p] = a.topk_idx[t0 * k + p];
+    for (int p = tid; p < nt * k; p += kThreads) s_id[p] = a.topk_idx[t0 * k + p];
     __syncthreads();
     const int pairs = T * k, own = t0 * k, quads = pairs / 4;
     auto count = [&](int p, int e) {
@@ -123,23 +123,28 @@ __global__ __launch_bounds__(kThreads) void k_dispatch_direct(DispatchArgs a, Di
         for (int g = tid; g <= a.groups; g += kThreads)
             a.group_offsets[g] = s_off[g * (E / a.groups)];
 
-    for (int i = 0; i < nt; i++) {
-        for (int j = tid; j < k; j += kThreads) {
-            const int p = (t0 + i) * k + j, e = s_row[i * k + j];
-            int r = -1;
-            if ((unsigned)e < (unsigned)E) {
-                r = (int)atomicAdd(&s_run[e], 1u);
-                if (r < 0 || r >= a.max_rows) r = -1;        // never write outside
+    for (int p = tid; p < nt * k; p += kThreads) {
+        const int e = s_id[p];
+        int r = -1;
+        if ((unsigned)e < (unsigned)E) {
+            // the earlier slots of this workgroup's tokens with the same expert
+            int rank = 0;
+            for (int q = 0; q < p; q += 4) {
+                const int4 v = *reinterpret_cast<const int4*>(s_id + q);
+                rank += (v.x == e) + (v.y == e && q + 1 < p) + (v.z == e && q + 2 < p) +
+                        (v.w == e && q + 3 < p);
             }
-            s_row[i * k + j] = r;
-            a.dst_row[p] = r;
-            if (r >= 0) {
-                a.row_src[r] = p;
-                if (a.scales == 1) a.out_scales[r] = a.x_scales[t0 + i];
-            }
+            r = (int)s_run[e] + rank;
+            if (r < 0 || r >= a.max_rows) r = -1;            // never write outside
         }
-        __syncthreads();                   // the next token's rows follow this one's
+        s_row[p] = r;
+        a.dst_row[own + p] = r;
+        if (r >= 0) {
+            a.row_src[r] = own + p;
+            if (a.scales == 1) a.out_scales[r] = nt == 1 ? first_scale : a.x_scales[t0 + p / k];
+        }
     }
+    __syncthreads();
     for (int i = wave; i < nt * CW; i += kWaves) {
         const int t = i / CW, u = (i % CW) * kWave + lane;
         if (i != wave) piece = load(i);
@@ -178,22 +183,34 @@ bool dispatch_direct_applies(int64_t T, int k) { return T * k <= kDirectPairs; }
 hipError_t launch_dispatch_direct(const DispatchArgs& a, hipStream_t stream, LaunchInfo* info,
                                   bool run) {
     DirectPlan plan;
-    // one workgroup a token while all of them run at once (four a CU), then more tokens
-    // each, since every workgroup counts the whole table: 2777 tokens x 6 of 60 experts,
-    // 1408 bytes, us: 1024 workgroups 15.4, 512 16.1, 2048 19.1
-    int64_t tokens = (a.T + kBlocks - 1) / kBlocks;
+    // One workgroup a token while all of them run at once, then more tokens each, since
+    // every workgroup counts the whole table. Up to 768 tokens four workgroups of 512
+    // threads a CU, then two of 1024, which count half as often. us, tokens x choices of
+    // experts, bytes a row:             4 of 512  2 of 1024
+    //     128 x 8 of 256, 7168             5.8       6.0
+    //     700 x 8 of 128, 2048             7.6       7.7
+    //    1024 x 8 of 256, 1024             8.8       8.1
+    //    2777 x 6 of 60, 1408, 16-row     14.8      12.2
+    //    4096 x 8 of 256, 1024            17.5      14.9
+    //   32768 x 1 of 8, 512               35.4      25.2
+    const bool wide = a.T > 768;
+    const int most = wide ? 512 : 1024;
+    int64_t tokens = (a.T + most - 1) / most;
     if (tokens * a.k > kRowSlots) tokens = kRowSlots / a.k;
     plan.tokens = tokens < 1 ? 1 : (int)tokens;
     plan.pad_per_expert = a.T > 0 && a.row_align > 1 ? (a.row_align - 1 < 4 ? a.row_align - 1 : 4) : 0;
     plan.pad_parts = a.E * plan.pad_per_expert;
     plan.pad_rows = plan.pad_parts ? (a.row_align + plan.pad_per_expert - 2) / plan.pad_per_expert : 0;
     const int64_t token_blocks = (a.T + plan.tokens - 1) / plan.tokens;
-    const int64_t least = plan.pad_parts < kBlocks ? plan.pad_parts : kBlocks;
+    const int64_t least = plan.pad_parts < most ? plan.pad_parts : most;
     plan.blocks = (int)(token_blocks > least ? token_blocks : least);
     if (plan.blocks < 1) plan.blocks = 1;              // no tokens: the tables
-    if (info) *info = LaunchInfo{plan.blocks, kThreads, 0, plan.tokens, "count+scan+scatter"};
+    const int threads = wide ? 1024 : 512;
+    if (info) *info = LaunchInfo{plan.blocks, threads, 0, plan.tokens, "count+scan+scatter"};
     if (!run) return hipSuccess;
-    k_dispatch_direct<<<dim3((unsigned)plan.blocks), dim3(kThreads), 0, stream>>>(a, plan);
+    const dim3 grid((unsigned)plan.blocks), block(threads);
+    if (wide) k_dispatch_direct<1024><<<grid, block, 0, stream>>>(a, plan);
+    else k_dispatch_direct<512><<<grid, block, 0, stream>>>(a, plan);
     return hipGetLastError();
 }
 
