@@ -103,6 +103,7 @@ def check(c, act, off=None):
     ([0, 0, 3], 2032, 64), ([16, 17, 31, 32, 33], 512, 304), ([64, 65, 127, 128], 384, 256),
     ([129, 1, 255], 640, 512), ([300, 700], 272, 768), ([1000], 1024, 1032), ([2] * 40, 528, 128),
     ([257, 0, 0, 513], 128, 272), ([4096], 256, 256), ([1] * 600, 128, 32), ([40], 112, 24),
+    ([1] * 1024, 16, 8), ([0] * 1023 + [70], 32, 16),
 ])
 @pytest.mark.parametrize("gated", [False, True])
 def test_segments_and_sizes(counts, K, N, gated):

@@ -169,6 +169,20 @@ def test_largest_weights_and_x_as_its_own_residual():
         check(x, x, w, quant)
 
 
+def test_least_alignment():
+    """Codes at a multiple of 8 bytes, scales at one of 4, the rest at 16."""
+    from combine_moe_route_amd import moe_rmsnorm_quant
+    log("rmsnorm alignment")
+    x, res, w = make(21, 1032, True, 8)
+    ref = run(x, res, w, "int8")
+    out = torch.zeros(21 * 1032 + 8, dtype=torch.int8, device=DEV)[8:].view(21, 1032)
+    sc = torch.zeros(22, device=DEV)[1:]
+    sums = torch.zeros(21 * 1032 + 8, dtype=torch.bfloat16, device=DEV)[8:].view(21, 1032)
+    assert out.data_ptr() % 16 == 8 and sc.data_ptr() % 8 == 4
+    moe_rmsnorm_quant(x, w, residual=res, sum_out=sums, out=out, out_scales=sc)
+    assert torch.equal(out, ref[0]) and torch.equal(sc, ref[1]) and torch.equal(sums, ref[3])
+
+
 def test_many_short_rows():
     log("rmsnorm many rows")
     check(*make(300_001, 8, True, 4), "int8")
