@@ -62,7 +62,8 @@ def check(h, off, act):
     (9, 512, [0, 8]), (513, 528, [0, 500, 513]), (70, 1040, [0, 70]), (64, 2048, [0, 0]),
     (21, 2048, [0, 4, 100]), (6, 2064, [0, 6]), (33, 4096, [0, 31]), (5, 4112, [0, 5]),
     (4, 8192, [0, 4]), (3, 8208, [0, 3]), (3, 18432, [0, 2]), (2, 32768, [0, 2]),
-    (3000, 640, [0, 1, 2999]),
+    (3000, 640, [0, 1, 2999]), (1100, 2048, [0, 1099]), (1500, 1040, [0, 700, 1500]),
+    (1023, 1536, [0, 1023]), (1024, 1536, [0, 1024]), (1200, 2064, [0, 1200]),
 ])
 def test_sizes(act, R, I, off):
     log(f"gated_act_int8 {act} R={R} I={I}")
@@ -70,12 +71,11 @@ def test_sizes(act, R, I, off):
     check(torch.randn((R, 2 * I), device=DEV, generator=gen).to(torch.bfloat16), off, act)
 
 
-@pytest.mark.parametrize("I", [64, 512, 4096, 16384])
-def test_values(I):
+@pytest.mark.parametrize("I,R", [(64, 24), (512, 24), (2048, 24), (2048, 1100), (4096, 24), (16384, 24)])
+def test_values(I, R):
     """Zero rows, one large value in a row, tiny and huge rows, large gates of
     either sign, products past fp32's range, rows behind the end that hold NaN."""
-    log(f"gated_act_int8 values I={I}")
-    R = 24
+    log(f"gated_act_int8 values I={I} R={R}")
     gen = torch.Generator(DEV).manual_seed(3)
     h = torch.randn((R, 2 * I), device=DEV, generator=gen).to(torch.bfloat16)
     h[0] = 0
