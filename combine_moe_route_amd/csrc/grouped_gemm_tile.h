@@ -670,11 +670,14 @@ template <typename P, typename SH>
 hipError_t launch_shape(const GroupedGemmArgs& g, hipStream_t stream, LaunchInfo* info, bool run) {
     const int n_out = g.gated ? g.N / 2 : g.N;
     const int out_cols = g.gated ? SH::kBN / 2 : SH::kBN;
-    // m segments that have rows hold at most m + (max_rows - m) / kBM tiles. A tile that
-    // no segment has costs a workgroup that finds this out: with max_rows / kBM + E
-    // tiles, 1 token through 2 of 8 experts launched four times what it needed.
+    // m segments that have rows, and do not overlap, hold at most m + (max_rows - m) / kBM
+    // tiles. A tile that no segment has costs a workgroup that finds this out: with
+    // max_rows / kBM + E tiles, 1 token through 2 of 8 int8 experts (K 4096, N 16384)
+    // launched four times what it needed, 26.5 us instead of 24.2. The bf16 product's
+    // interface does not exclude segments that overlap, so its grid has room for some.
     const int64_t m = g.E < g.max_rows ? g.E : g.max_rows;
-    const int64_t max_tiles = m + (g.max_rows - m) / SH::kBM;
+    const int64_t max_tiles = P::kScaled ? m + (g.max_rows - m) / SH::kBM
+                                         : (g.max_rows + SH::kBM - 1) / SH::kBM + g.E;
     const int64_t items = max_tiles * ((n_out + out_cols - 1) / out_cols);
     const int64_t grid = (items + kXcds - 1) / kXcds * kXcds;
     constexpr bool kSkinny = SH::kBN <= 64;

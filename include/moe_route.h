@@ -513,7 +513,9 @@ int moe_gated_act_quant_fp8(const void* h, const int32_t* expert_offsets, int E,
  *   a               device int8 [max_rows, K], 16-byte aligned
  *   a_scales        device fp32 [max_rows]
  *   expert_offsets  device int32 [E+1]: moe_dispatch_quantized's expert_offsets
- *                   (any row_align). Segment bounds are clamped to [0, max_rows]
+ *                   (any row_align). Segment bounds are clamped to [0, max_rows],
+ *                   a pair that descends is an empty segment, and segments do not
+ *                   overlap
  *   w               device int8 [E, N, K], K contiguous, 16-byte aligned
  *   w_scales        device fp32 [E, N], 16-byte aligned
  *   bias            device bf16 [E, N], 16-byte aligned, or NULL
