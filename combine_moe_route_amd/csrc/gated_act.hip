@@ -46,10 +46,19 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 // differ from those of 64-bit arithmetic with silu and 39 to 60 with gelu (the
 // rounding of s alone moves most of them); fp32 with the library's exp, erf and
 // divisions 32 to 51 and 64 to 93.
-template <int ACT>
+//
+// With KEEP_NAN a NaN u stays one next to a gate whose activation is 0, by a product
+// with that 0 (g u past fp32 then is NaN too, which the INT8 kernel's second pass
+// resolves). Without, for finite rows, the 0 is chosen as the result: +0, whose code
+// has no sign. Either way takes as many instructions; a 0 u added to the selection
+// took FP8 silu from 239 to 244 us (147 thousand rows of 2048).
+template <int ACT, bool KEEP_NAN>
 __device__ __forceinline__ float gated_product(float g, float u) {
     const float p = g * u;
-    if constexpr (ACT == kActRelu) return g < 0.0f ? 0.0f : p;
+    if constexpr (ACT == kActRelu) {
+        if constexpr (KEEP_NAN) return (g < 0.0f ? 0.0f : g) * u;
+        return g < 0.0f ? 0.0f : p;
+    }
     if constexpr (ACT == kActSilu) {
         float e = __builtin_amdgcn_exp2f(-1.44268798828125f * g);
         e = fmaf(e, -4.88849515e-06f * g, e);            // (log2 e - the above) ln 2
@@ -58,6 +67,7 @@ __device__ __forceinline__ float gated_product(float g, float u) {
         r = fmaf(fmaf(-d, r, 1.0f), r, r);
         // d is inf for g below -88.7; it stays NaN for a NaN gate. A reciprocal below
         // 2^-126 (g below -87.3) may count as 0.
+        if constexpr (KEEP_NAN) return p * (d == INFINITY ? 0.0f : r);
         return d == INFINITY ? 0.0f : p * r;
     }
     if constexpr (ACT == kActGelu) {
@@ -112,7 +122,7 @@ __global__ __launch_bounds__(kGatedThreads) void k_gated_act_fp8(
 #pragma unroll
             for (int i = 0; i < 8; i++) {
                 pmax = fmaxf(pmax, fabsf(g[i] * v[i]));
-                v[i] = gated_product<ACT>(g[i], v[i]);
+                v[i] = gated_product<ACT, false>(g[i], v[i]);
                 amax = fmaxf(amax, fabsf(v[i]));
             }
             // g u out of range: act(g) u maybe not. If it is, the largest finite value
@@ -220,7 +230,7 @@ __global__ __launch_bounds__(S > 256 ? S : 256) void k_gated_act_int8(
         unpack8(make_uint4(u4[i][0], u4[i][1], u4[i][2], u4[i][3]), v[i]);
 #pragma unroll
         for (int z = 0; z < 8; z++) {
-            v[i][z] = gated_product<ACT>(g[z], v[i][z]);
+            v[i][z] = gated_product<ACT, true>(g[z], v[i][z]);
             most = __builtin_elementwise_maximum(most, fabsf(v[i][z]));
         }
     }
