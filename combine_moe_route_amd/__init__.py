@@ -9,6 +9,8 @@ The binding is imported on first use of any API name, so building the
 library never needs an existing one; using the API without the library
 raises ImportError.
 """
+import types
+
 _API = (
     "DispatchBuffers",
     "MoeRouteError",
@@ -39,6 +41,25 @@ _API = (
 )
 
 __all__ = list(_API)
+
+
+def _forget(names, held):
+    """Drop the names that still stand here as `held`, the binding's namespace, has them."""
+    for name in names:
+        if name in _API and name in held and globals().get(name) is held[name]:
+            del globals()[name]
+
+
+class _Binding(types.ModuleType):
+    """The binding's class: a name that is replaced there is looked up again here."""
+
+    def __setattr__(self, name, value):
+        _forget((name,), vars(self))
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        _forget((name,), vars(self))
+        super().__delattr__(name)
 
 
 def __getattr__(name):

@@ -11,9 +11,17 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from typing import NamedTuple, Optional
 
 import torch
+
+from . import _API, _Binding, _forget
+
+# the package keeps the names it has looked up here, until they are replaced or
+# this module is loaded again
+_forget(_API, globals())
+sys.modules[__name__].__class__ = _Binding
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("MOE_ROUTE_LIB", os.path.join(_HERE, "libmoeroute.so"))
