@@ -199,7 +199,7 @@ int dispatch_impl(const float* logits, float* topk_w, const void* x, const int32
     int nk = 0;
     // geometry (route_sort_applies looks only at the logits address)
     auto launch = [&](hipStream_t on, bool go) {
-        if (scales > 0 && moe::dispatch_direct_applies(T, k)) {
+        if (scales > 0 && moe::dispatch_direct_applies(T, E, k)) {
             nk = 1;
             return moe::launch_dispatch_direct(a, on, info, go);
         }

@@ -15,8 +15,8 @@
 // of 256 experts 8.3 -> 4.8, 128 tokens 9.9 -> 5.7 (one launch instead of two); 2777
 // tokens of 1408 bytes to 6 of 60, 16-row segments 19.6 -> 12.2, 4096 tokens of 1024
 // to 8 of 256 21.2 -> 14.9 (instead of three). What is left is counting (in every
-// workgroup, about 4 us at 16 thousand slots) next to the copy. Past 32768 slots the
-// counters' halves could overflow.
+// workgroup, about 4 us at 16 thousand slots) next to the copy. Slots of one expert
+// are counted one after the other, so the routing matters; see the rule below.
 #include "launch.h"
 #include "moe_device.h"
 
@@ -178,7 +178,27 @@ __global__ __launch_bounds__(kThreads) void k_dispatch_direct(DispatchArgs a, Di
 
 }  // namespace
 
-bool dispatch_direct_applies(int64_t T, int k) { return T * k <= kDirectPairs; }
+// Up to kDirectPairs slots (the counters' halves hold 65535), and no more than 2048 an
+// expert on average, or 4096 with one choice a token, where the kernels have more tokens
+// to pass over. us here / by the counting, scanning and copying kernels, rows of 512 bytes,
+// popularity of a spread of 0.5:
+//   slots        4096         8192        16384        32768
+//   1 of 1     12.1/13.2    19.8/15.3    34.9/21.2    66.8/33.4
+//   1 of 4      9.4/13.3    14.5/15.7    24.9/21.7    45.8/34.1
+//   1 of 8      7.9/13.4    11.0/15.7    17.9/21.7    31.9/34.5
+//   2 of 2     10.7/9.3     17.0/13.9    29.3/16.7    54.5/23.0
+//   2 of 8      7.7/9.5     10.5/14.3    16.3/17.1    28.2/23.7
+//   4 of 8      7.6/9.7      9.9/10.2    14.5/15.5    24.1/19.2
+//   8 of 8      6.6/10.2     9.4/11.1    13.1/11.9    20.8/17.8
+//   8 of 16     6.3/10.1     8.7/11.0    11.8/11.9    17.9/17.7
+//   8 of 32     6.0/10.1     8.3/11.2    11.0/12.0    15.9/17.8
+// The host does not know how the slots are spread: 32768 x 1 of 8 take 24.5 (evenly), 51
+// (popularity of a spread of 3) or 67 (all to one) against 34; 4096 x 8 of 256, rows of
+// 1024, 14.6 or 19.8 against 19.4. With 48 to 65 thousand slots what is gained shrinks
+// (8191 x 8 of 256, rows of 1024: 26.0/29.4; of 32: 30.1/28.9).
+bool dispatch_direct_applies(int64_t T, int E, int k) {
+    return T * k <= kDirectPairs && T * k <= (k == 1 ? 4096 : 2048) * (int64_t)E;
+}
 
 hipError_t launch_dispatch_direct(const DispatchArgs& a, hipStream_t stream, LaunchInfo* info,
                                   bool run) {

@@ -83,10 +83,10 @@ DispatchWorkspace dispatch_workspace(int64_t T, int E, int k);
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t stream, LaunchInfo info[4], int* n,
                            bool run = true);
 
-// Rows already quantised (scales > 0), at most kDirectPairs slots: one kernel that
-// needs no workspace.
+// Rows already quantised (scales > 0), at most kDirectPairs slots that are not too many
+// for their experts: one kernel that needs no workspace.
 constexpr int64_t kDirectPairs = 32768;
-bool dispatch_direct_applies(int64_t T, int k);
+bool dispatch_direct_applies(int64_t T, int E, int k);
 hipError_t launch_dispatch_direct(const DispatchArgs& a, hipStream_t stream, LaunchInfo* info,
                                   bool run = true);
 
