@@ -24,7 +24,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kRowSlots = 2048;            // slots of a workgroup's tokens
+constexpr int kRowSlots = kMaxExperts;     // slots of a workgroup's tokens, at most
 constexpr int kBatch = 4;                  // 16-byte loads of the table in flight
 
 // Four slots of the table, which is aligned to one.
@@ -215,8 +215,9 @@ hipError_t launch_dispatch_direct(const DispatchArgs& a, hipStream_t stream, Lau
     //   32768 x 1 of 8, 512               35.4      25.2
     const bool wide = a.T > 768;
     const int most = wide ? 512 : 1024;
-    int64_t tokens = (a.T + most - 1) / most;
-    if (tokens * a.k > kRowSlots) tokens = kRowSlots / a.k;
+    // Slots of a workgroup: k of one token, at most kMaxExperts; or, past 768 tokens,
+    // where k <= 32768 / 769, fewer than k (T / 512 + 1) <= 64 + 42.
+    const int64_t tokens = (a.T + most - 1) / most;
     plan.tokens = tokens < 1 ? 1 : (int)tokens;
     plan.pad_per_expert = a.T > 0 && a.row_align > 1 ? (a.row_align - 1 < 4 ? a.row_align - 1 : 4) : 0;
     plan.pad_parts = a.E * plan.pad_per_expert;
