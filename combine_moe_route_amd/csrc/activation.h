@@ -1,5 +1,6 @@
-// Activations shared by the bf16 grouped GEMM's epilogue and the gated
-// activation between the FP8 products. fp32 throughout.
+// Activations of the bf16 and INT8 grouped GEMMs' epilogue and of the gated activations
+// between two products (FP8, INT8), in fp32 throughout; and the rounding to bf16 that
+// these and the quantising norm share.
 #pragma once
 
 #include "moe_device.h"

@@ -701,8 +701,9 @@ struct RowScales {
 // in through scalar loads; the x row is read once through a range descriptor (lanes
 // past the row read zeros) and stored to each of the token's rows. Quantised rows
 // are stored with the non-temporal hint (16384 tokens of 7168 bytes to 8 of 256
-// experts, 128-row segments, the whole dispatch: 257 -> 230 us; 224 with the pad
-// blocks among the others; 5.3 TB/s, where a fill runs at 6.9).
+// experts, 128-row segments, the whole dispatch: 257 -> 230 us; 220 with the pad
+// blocks among the others; 5.4 TB/s, where a fill runs at 6.9). That is with x in the
+// cache, as just written; 242 to 250 us, 4.9 TB/s, if x comes from memory.
 template <int MODE, int KL, bool SCALED>
 __global__ __launch_bounds__(kScatterThreads) void k_scatter_rows(
     const uint16_t* __restrict__ x, const int32_t* __restrict__ topk_idx,

@@ -321,6 +321,8 @@ int moe_dispatch_quantized(const void* x, const float* x_scales, const int32_t* 
  *   eps          1e-30 <= eps <= 1
  *   T >= 0 (T == 0 is a no-op), T * ld_x <= 2^40, ld_x <= 2^31; the launch has to
  *   fit a packet (T * 1024 < 2^32 always does)
+ * h * weight is formed first, then multiplied by the root's reciprocal; a product
+ * below 2^-126 has fewer bits (a step of 2^-149).
  * A token with an infinity or NaN in h (also one that the addition made) gets NaN
  * in y and in its scales and zero codes. Outputs overlap neither inputs nor each
  * other, but for sum == residual (MOE_EINVAL; the gaps between rows of x are free).
@@ -549,6 +551,7 @@ int moe_grouped_gemm_int8(const void* a, const float* a_scales, const int32_t* e
  *   h               device bf16 [max_rows, 2 I], 16-byte aligned, no infinities:
  *                   the y of moe_grouped_gemm_int8 with N = 2 I (gate, then up).
  *                   A row that holds a NaN in v gets the scale NaN and zero codes
+ *                   (also a NaN of the up half where act(h[r, c]) is 0)
  *   expert_offsets  device int32 [E+1]; only [E] is read
  *   out             device int8 [max_rows, I] out, 16-byte aligned
  *   out_scales      device fp32 [max_rows] out
